@@ -77,6 +77,7 @@ extern "C" {
 #define PKV_DEV_BAD_LENGTH  0x4  /* context_len < 0, > 16 * table width, or > max_context_len */
 #define PKV_DEV_TIMEOUT     0x8  /* a bounded wait on a bulk copy ran out               */
 #define PKV_DEV_BAD_PREFIX  0x10 /* cascade decode: a table does not start with the shared prefix */
+#define PKV_DEV_BAD_POSITION 0x20 /* kv_append_rope: a position outside the rotation's table */
 
 typedef struct pkv_pool* pkv_pool_t;   /* opaque host-side handle */
 
@@ -162,6 +163,47 @@ PKV_API size_t kv_append_workspace_bytes(pkv_pool_t pool, int num_tokens);
 PKV_API int kv_append(pkv_pool_t pool, int layer, const void* k, const void* v, int src_dtype,
               const int32_t* slot_mapping, int num_tokens,
               void* workspace, size_t workspace_bytes, void* stream);
+
+/* The rotation of kv_append_rope (rotary position encoding). */
+typedef struct {
+    const float* cos_sin;      /* [device] fp32 [max_positions][rotary_dim], 16-byte aligned: row p holds
+                                  cos(p * w_i) for i < rotary_dim / 2, then sin(p * w_i) */
+    int32_t max_positions;     /* rows of the table, > 0 */
+    int32_t rotary_dim;        /* the first rotary_dim dims of a head are rotated, the others kept: a
+                                  multiple of 16 in [16, head_dim] */
+    int32_t interleaved;       /* 0: dims i and i + rotary_dim / 2 are a pair; 1: dims 2i and 2i + 1 */
+} pkv_rope;
+
+/* Workspace kv_append_rope needs for num_tokens tokens: 0 for 16-bit pools and for up to 512
+ * tokens; else 4 bytes per slot of the pool (its contents need no initialization). */
+PKV_API size_t kv_append_rope_workspace_bytes(pkv_pool_t pool, int num_tokens);
+
+/*
+ * kv_append_rope -- kv_append with the position rotation applied on the way ([KVB] "The KV
+ * cache": keys never change once cached, so they are cached rotated).  With the angles of the
+ * token's position, every pair (x1, x2) of q's and k's heads becomes
+ *     y1 = x1 cos - x2 sin,   y2 = x2 cos + x1 sin
+ * in IEEE fp32, each operation rounded, then once to src_dtype.  q goes to q_out; k and v go to
+ * the slots exactly as kv_append stores rows of src_dtype (16-bit pools: a byte copy, src_dtype
+ * equal to the pool dtype; quantized pools: kv_append's quantization, src_dtype PKV_F16 or PKV_BF16).
+ *   q [device]: rows of [num_q_heads][head_dim]; k, v: rows of [num_kv_heads][head_dim].  Token t's
+ *        row starts q_stride (k_stride, v_stride) elements times t into it, so q, k and v may be
+ *        parts of one projection's output.  16-byte aligned, strides multiples of 8 elements.
+ *        num_q_heads 0 rotates k only (q and q_out may be NULL, their strides 0).
+ *   q_out [device]: rows as q with stride q_out_stride; may be q itself with the same stride,
+ *        else it must not overlap an input.
+ *   positions [device]: int32 [num_tokens], in [0, rope->max_positions).
+ *   slot_mapping [device]: int32 [num_tokens].  A token with a negative slot is padding: nothing
+ *        is read or written for it, its q_out row included.  Two tokens of one call must not
+ *        share a slot.
+ *   workspace [device]: kv_append_rope_workspace_bytes(pool, num_tokens) bytes.
+ * A token whose slot or position is out of range is skipped like padding and sets
+ * PKV_DEV_BAD_SLOT or PKV_DEV_BAD_POSITION.
+ */
+PKV_API int kv_append_rope(pkv_pool_t pool, int layer, const void* q, int64_t q_stride, const void* k,
+                           int64_t k_stride, const void* v, int64_t v_stride, int src_dtype, const pkv_rope* rope,
+                           const int32_t* positions, const int32_t* slot_mapping, int num_tokens, int num_q_heads,
+                           void* q_out, int64_t q_out_stride, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Tuning options for paged_decode_attn (NULL = defaults). */
 typedef struct {

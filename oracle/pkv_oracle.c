@@ -365,7 +365,7 @@ int orc_kv_append(int N, int H_kv, int d, int dtype,
         }
         return ORC_OK;
     }
-    if (src_dtype != ORC_BF16 || !k_scale || !v_scale)
+    if ((src_dtype != ORC_BF16 && src_dtype != ORC_F16) || !k_scale || !v_scale)
         return ORC_ERR_DTYPE;
     int rc = append_quantized(N, H_kv, d, dtype, k_pool, k_scale, k_src, src_dtype, slots, T);
     if (rc != ORC_OK) return rc;

@@ -310,6 +310,71 @@ int kv_append(pkv_pool_t pool, int layer, const void* k, const void* v, int src_
     return launch_append(a, static_cast<cudaStream_t>(stream));
 }
 
+size_t kv_append_rope_workspace_bytes(pkv_pool_t pool, int num_tokens)
+{
+    if (!pool || num_tokens < 0) return 0;
+    return append_rope_workspace_bytes(pool->d.num_blocks, pool->d.kv_dtype, num_tokens);
+}
+
+int kv_append_rope(pkv_pool_t pool, int layer, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                   const void* v, int64_t v_stride, int src_dtype, const pkv_rope* rope, const int32_t* positions,
+                   const int32_t* slot_mapping, int num_tokens, int num_q_heads, void* q_out, int64_t q_out_stride,
+                   void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (!pool || !rope) return PKV_ERR_NULL;
+    const pkv_pool_desc& d = pool->d;
+    if (layer < 0 || layer >= d.num_layers || num_tokens < 0 || num_q_heads < 0) return PKV_ERR_ARG;
+    if (rope->rotary_dim < 16 || rope->rotary_dim > d.head_dim || rope->rotary_dim % 16) return PKV_ERR_SHAPE;
+    if (rope->max_positions <= 0 || rope->interleaved < 0 || rope->interleaved > 1) return PKV_ERR_ARG;
+    if (src_dtype != PKV_F16 && src_dtype != PKV_BF16) return PKV_ERR_DTYPE;
+    if (!is_quantized(d.kv_dtype) && src_dtype != d.kv_dtype) return PKV_ERR_DTYPE;
+    const int64_t q_row = (int64_t)num_q_heads * d.head_dim, kv_row = (int64_t)d.num_kv_heads * d.head_dim;
+    if (k_stride < kv_row || v_stride < kv_row || q_stride < q_row || q_out_stride < q_row) return PKV_ERR_SHAPE;
+    if (num_tokens == 0) return PKV_OK;
+    if (!k || !v || !positions || !slot_mapping || !rope->cos_sin || (num_q_heads > 0 && (!q || !q_out)))
+        return PKV_ERR_NULL;
+    // 16-byte accesses: aligned bases, strides of whole 8-element chunks
+    const uintptr_t bases = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
+                            reinterpret_cast<uintptr_t>(rope->cos_sin) |
+                            (num_q_heads > 0 ? reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(q_out) : 0);
+    if ((bases & 15) || ((k_stride | v_stride | (num_q_heads > 0 ? q_stride | q_out_stride : 0)) & 7)) return PKV_ERR_ARG;
+    // one CTA per token and row group: the grid stays below 2^31
+    if ((long long)num_tokens * (num_q_heads + 2LL * d.num_kv_heads + 1) > 0x7fffffffLL / 2) return PKV_ERR_ARG;
+    const size_t need = append_rope_workspace_bytes(d.num_blocks, d.kv_dtype, num_tokens);
+    if (need && (!workspace || workspace_bytes < need)) return PKV_ERR_WORKSPACE;
+    if (need && (reinterpret_cast<uintptr_t>(workspace) & 3)) return PKV_ERR_ARG;
+    AppendArgs a;
+    a.k = k;
+    a.v = v;
+    a.slots = slot_mapping;
+    a.T = num_tokens;
+    a.N = d.num_blocks;
+    a.H_kv = d.num_kv_heads;
+    a.d = d.head_dim;
+    a.kv_dtype = d.kv_dtype;
+    a.k_pool = pool->k_base[layer];
+    a.v_pool = pool->v_base[layer];
+    a.k_scale = pool->ks_base[layer];
+    a.v_scale = pool->vs_base[layer];
+    a.workspace = workspace;
+    a.status = d.device_status;
+    RopeArgs r;
+    r.q = q;
+    r.q_out = q_out;
+    r.q_stride = q_stride;
+    r.k_stride = k_stride;
+    r.v_stride = v_stride;
+    r.q_out_stride = q_out_stride;
+    r.table = rope->cos_sin;
+    r.positions = positions;
+    r.src_dtype = src_dtype;
+    r.H_q = num_q_heads;
+    r.rotary_dim = rope->rotary_dim;
+    r.interleaved = rope->interleaved;
+    r.max_positions = rope->max_positions;
+    return launch_append_rope(a, r, static_cast<cudaStream_t>(stream));
+}
+
 // CTAs the decode grid has per (sequence, partition): one per KV head and group of 16 query heads.
 static int ctas_per_partition(pkv_pool_t pool, int num_q_heads)
 {

@@ -22,10 +22,9 @@
 //      stores s.  Another row of the same block may read the scale before or after that
 //      store: max(S_old, amax/Q) and max(s, amax/Q) are both s, so the result is the same.
 // All arithmetic is IEEE fp32 with explicit round-to-nearest operations (no fast math).
-#include <cuda_fp8.h>
-
 #include "common.cuh"
 #include "internal.h"
+#include "quant_codes.cuh"
 
 namespace pkv {
 
@@ -138,46 +137,6 @@ __global__ void qappend_reduce_kernel(const __nv_bfloat16* __restrict__ k, const
         atomicMax(&q.amax_k[(size_t)blk * H_kv + h], __float_as_uint(ak));
         atomicMax(&q.amax_v[(size_t)blk * H_kv + h], __float_as_uint(av));
         if (h == 0) atomicOr(&q.mask[blk], 1u << (slot % kBlock));
-    }
-}
-
-// Code of x / s for storage dtype DT, IEEE fp32 round-to-nearest throughout.
-template <int DT>
-__device__ __forceinline__ uint32_t quant_code(float x, float s)
-{
-    if (s == 0.f) return 0u;
-    const float r = __fdiv_rn(x, s);
-    if constexpr (DT == PKV_FP8E4M3) {
-        return (uint32_t)__nv_cvt_float_to_fp8(r, __NV_SATFINITE, __NV_E4M3);
-    } else {
-        constexpr float Q = DT == PKV_INT8 ? 127.f : 7.f;
-        const float c = fminf(fmaxf(rintf(r), -Q), Q);
-        return (uint32_t)(int)c & (DT == PKV_INT8 ? 0xffu : 0xfu);
-    }
-}
-
-template <int DT>
-__device__ __forceinline__ float code_value(uint32_t c)
-{
-    if constexpr (DT == PKV_FP8E4M3) {
-        return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)c, __NV_E4M3)));
-    } else if constexpr (DT == PKV_INT8) {
-        return (float)(int)(int8_t)c;
-    } else {
-        return (float)(((int)c ^ 8) - 8);   // 4-bit two's complement
-    }
-}
-
-template <int DT>
-__device__ __forceinline__ uint32_t requant_code(uint32_t c, float s_old, float s)
-{
-    const float r = __fdiv_rn(__fmul_rn(code_value<DT>(c), s_old), s);
-    if constexpr (DT == PKV_FP8E4M3) {
-        return (uint32_t)__nv_cvt_float_to_fp8(r, __NV_SATFINITE, __NV_E4M3);
-    } else {
-        constexpr float Q = DT == PKV_INT8 ? 127.f : 7.f;
-        const float q = fminf(fmaxf(rintf(r), -Q), Q);
-        return (uint32_t)(int)q & (DT == PKV_INT8 ? 0xffu : 0xfu);
     }
 }
 

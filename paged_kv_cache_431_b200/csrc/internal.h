@@ -84,6 +84,19 @@ struct AppendArgs {
 int launch_append(const AppendArgs& a, cudaStream_t s);
 size_t append_workspace_bytes(int N, int H_kv, int kv_dtype);
 
+// What kv_append_rope takes beyond AppendArgs; strides in elements per token.
+struct RopeArgs {
+    const void* q;
+    void* q_out;
+    int64_t q_stride, k_stride, v_stride, q_out_stride;
+    const float* table;
+    const int32_t* positions;
+    int src_dtype, H_q, rotary_dim, interleaved, max_positions;
+};
+
+int launch_append_rope(const AppendArgs& a, const RopeArgs& r, cudaStream_t s);
+size_t append_rope_workspace_bytes(int N, int kv_dtype, int T);
+
 struct PrefillArgs {
     const void* q;
     int q_dtype;

@@ -19,6 +19,7 @@ MAX_LAYERS = 256          # PKV_MAX_LAYERS
 F16, BF16, INT8, INT4, FP8E4M3 = 0, 1, 2, 3, 4
 QUANTIZED = (INT8, INT4, FP8E4M3)
 DEV_BAD_BLOCK, DEV_BAD_SLOT, DEV_BAD_LENGTH, DEV_TIMEOUT, DEV_BAD_PREFIX = 0x1, 0x2, 0x4, 0x8, 0x10
+DEV_BAD_POSITION = 0x20
 ENGINE_AUTO, ENGINE_MMA, ENGINE_FMA2, ENGINE_FMA = 0, 1, 2, 3
 
 _TORCH16 = {F16: torch.float16, BF16: torch.bfloat16}
@@ -39,6 +40,11 @@ class _PoolDesc(ctypes.Structure):
 
 class _DecodeOpts(ctypes.Structure):
     _fields_ = [("engine", ctypes.c_int32), ("partition_tokens", ctypes.c_int32), ("sliding_window", ctypes.c_int32)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("max_positions", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
 
 
 _lib = None
@@ -76,6 +82,11 @@ def lib() -> ctypes.CDLL:
     L.kv_append_workspace_bytes.argtypes = [P, i32]
     L.kv_append.restype = i32
     L.kv_append.argtypes = [P, i32, P, P, i32, P, i32, P, sz, P]
+    i64 = ctypes.c_int64
+    L.kv_append_rope_workspace_bytes.restype = sz
+    L.kv_append_rope_workspace_bytes.argtypes = [P, i32]
+    L.kv_append_rope.restype = i32
+    L.kv_append_rope.argtypes = [P, i32, P, i64, P, i64, P, i64, i32, P, P, P, i32, i32, P, i64, P, sz, P]
     L.paged_decode_workspace_bytes.restype = sz
     L.paged_decode_workspace_bytes.argtypes = [P, i32, i32, i32, P]
     L.paged_decode_attn.restype = i32
@@ -250,6 +261,113 @@ def kv_append(pool: KVPool, layer: int, k: torch.Tensor, v: torch.Tensor, slot_m
     _check(lib().kv_append(pool.handle, layer, _ptr(k), _ptr(v), _dtype_code(k), _ptr(slot_mapping), T,
                            _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None
                            else 0, _stream(stream)), "kv_append")
+
+
+class _OnDevice:
+    """What the calls below share: all tensors on one CUDA device, which is made current for the
+    launch if it is not; a workspace taken from torch's allocator stays reserved for the stream
+    that the call runs on."""
+
+    def __init__(self, device, stream, *tensors):
+        if device.type != "cuda":
+            raise ValueError("expected CUDA tensors")
+        for t in tensors:
+            if t is not None and t.device != device:
+                raise ValueError(f"tensors on {device} and {t.device}")
+        self.device = device
+        self.given = stream
+        self.before = None
+
+    def __enter__(self):
+        now = torch.cuda.current_device()
+        if self.device.index != now:
+            self.before = now
+            torch.cuda.set_device(self.device)
+        return self
+
+    def __exit__(self, *exc):
+        if self.before is not None:
+            torch.cuda.set_device(self.before)
+
+    def stream(self):
+        return _stream(self.given)
+
+    def empty(self, n: int):
+        ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        self.keep(ws)
+        return ws
+
+    def keep(self, t: torch.Tensor):
+        if self.given is not None:
+            s = self.given if hasattr(self.given, "cuda_stream") else torch.cuda.ExternalStream(int(self.given),
+                                                                                                 self.device)
+            t.record_stream(s)
+
+
+def _pool_device(pool: KVPool):
+    t = pool.k_data[0] if isinstance(pool.k_data, list) else pool.k_data
+    return t.device
+
+
+def _int32(t: torch.Tensor, n: int | None = None, what: str = "index tensor") -> ctypes.c_void_p:
+    if t.dtype != torch.int32 or not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise ValueError(f"{what}: expected a contiguous int32 tensor" + ("" if n is None else f" of {n} elements"))
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _rows(t: torch.Tensor, T: int, heads: int, d: int, what: str):
+    """(pointer, elements per token) of [T, heads, d] rows that are dense within a token."""
+    if t.shape != (T, heads, d) or (T and heads and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d))):
+        raise ValueError(f"{what}: expected [{T}, {heads}, {d}] with dense rows")
+    # a single token may carry any stride; it is not used
+    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if T > 1 else heads * d)
+
+
+def kv_append_rope_workspace_bytes(pool: KVPool, num_tokens: int) -> int:
+    return int(lib().kv_append_rope_workspace_bytes(pool.handle, num_tokens))
+
+
+def kv_append_rope(pool: KVPool, layer: int, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                   positions: torch.Tensor, cos_sin: torch.Tensor, slot_mapping: torch.Tensor,
+                   q_out: torch.Tensor | None = None, interleaved: bool = False,
+                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """Rotate q [T, H_q, head_dim] and k [T, H_kv, head_dim] by their tokens' positions (int32 [T])
+    and write k and v into slots slot_mapping (int32 [T]); returns the rotated q.
+
+    cos_sin: fp32 [max_positions, rotary_dim], a row's cosines, then its sines.  interleaved pairs
+    neighbouring dims instead of the halves.  q, k and v may be views of one projection's output
+    (dense within a token).  q_out may be q.  Rows of padding (negative slots) are not written.
+    q None appends only."""
+    T, d = slot_mapping.shape[0], pool.head_dim
+    dev = _pool_device(pool)
+    with _OnDevice(dev, stream, q, k, v, positions, cos_sin, slot_mapping, q_out, workspace) as on:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin: expected a contiguous fp32 [max_positions, rotary_dim] tensor")
+        H_q = 0 if q is None else q.shape[1]
+        kp, ks = _rows(k, T, pool.num_kv_heads, d, "k")
+        vp, vs = _rows(v, T, pool.num_kv_heads, d, "v")
+        qp = qop = None
+        qs = qos = 0
+        if k.dtype != v.dtype or (q is not None and q.dtype != k.dtype):
+            raise ValueError("q, k and v must have one dtype")
+        if q is not None:
+            qp, qs = _rows(q, T, H_q, d, "q")
+            if q_out is None:
+                q_out = torch.empty(T, H_q, d, dtype=q.dtype, device=dev)
+                on.keep(q_out)
+            if q_out.dtype != q.dtype:
+                raise ValueError("q_out must have q's dtype")
+            qop, qos = _rows(q_out, T, H_q, d, "q_out")
+        need = kv_append_rope_workspace_bytes(pool, T)
+        if need and workspace is None:
+            workspace = on.empty(need)
+        rope = _Rope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0)
+        _check(lib().kv_append_rope(pool.handle, layer, qp, qs, kp, ks, vp, vs, _dtype_code(k), ctypes.byref(rope),
+                                    _int32(positions, T, "positions"), _int32(slot_mapping, T, "slot_mapping"), T, H_q,
+                                    qop, qos, _ptr(workspace),
+                                    workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                    on.stream()), "kv_append_rope")
+    return q_out
 
 
 def _opts(engine: int, partition_tokens: int, sliding_window: int = 0):
