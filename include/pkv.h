@@ -322,6 +322,67 @@ PKV_API int paged_decode_attn_cascade(pkv_pool_t pool, int layer, const void* q,
                                       void* workspace, size_t workspace_bytes, const pkv_decode_opts* opts,
                                       void* stream);
 
+/* Workspace paged_decode_attn_groups needs for these sizes (bytes): per (sequence, query head) a
+ * head_dim + 2 fp32 partial for every partition of the longest prefix and the longest suffix. */
+PKV_API size_t paged_decode_groups_workspace_bytes(pkv_pool_t pool, int num_seqs, int num_q_heads, int num_groups,
+                                                   int max_group_size, int max_prefix_len, int max_suffix_len);
+
+/*
+ * paged_decode_attn_groups -- paged_decode_attn for a batch whose sequences come in groups, each
+ * group sharing a prefix of its own ([INF] "Prefix caching"; [KVG] "Prefix caching": a system
+ * prompt shared by every request; a server holds several).  Each prefix is read and attended once
+ * for the rows of its whole group, each sequence's other tokens on their own, and both are merged
+ * with the log-sum-exp rule; the result is the attention over the whole context.
+ *   q, out [device]: [num_seqs][num_q_heads][head_dim], both of q_dtype (PKV_F16 or PKV_BF16; for
+ *        16-bit pools the pool dtype), 16-byte aligned.  Sums and softmax are fp32, rounded once.
+ *   block_tables, context_lens [device]: as paged_decode_attn; every sequence's table starts with
+ *        its group's prefix blocks, and its context is at least the prefix.
+ *   group_starts [device]: int32 [num_groups + 1], ascending: group g is the sequences
+ *        group_starts[g] .. group_starts[g+1]-1.  Sequences of no group (behind the last) are
+ *        padding: their output rows are left as they are.
+ *   prefix_lens [device]: int32 [num_groups], multiples of 16; 0: the group shares nothing.
+ *   max_group_size, max_prefix_len, max_suffix_len [host]: bounds of a group's sequences, of
+ *        prefix_lens, and of context_len - prefix_len; they size the grids.
+ *   workspace [device]: paged_decode_groups_workspace_bytes(...) bytes, 16-byte aligned.
+ * All pool dtypes, head dims and group sizes.  On the device: lengths and group_starts out of
+ * range are clipped to the bounds and set PKV_DEV_BAD_LENGTH; a prefix that is no multiple of 16
+ * (it counts rounded down) or a table without its group's prefix sets PKV_DEV_BAD_PREFIX.
+ */
+PKV_API int paged_decode_attn_groups(pkv_pool_t pool, int layer, const void* q, int q_dtype,
+                                     const int32_t* block_tables, int block_table_width, const int32_t* context_lens,
+                                     int num_seqs, int num_q_heads, const int32_t* group_starts,
+                                     const int32_t* prefix_lens, int num_groups, int max_group_size,
+                                     int max_prefix_len, int max_suffix_len, float scale, void* out, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* Workspace paged_cross_attn needs for these sizes (bytes); 0 when no sequence's keys are split. */
+PKV_API size_t paged_cross_workspace_bytes(pkv_pool_t pool, int total_rows, int num_q_heads, int num_seqs,
+                                           int max_rows, int max_context_len);
+
+/*
+ * paged_cross_attn -- attention of a ragged batch of query rows to cached states of another
+ * length (a decoder's rows against its encoder's states; the K/V of the states were appended to
+ * the pool once and follow a block table like any sequence, [KVG] "PagedAttention").  Every row
+ * of sequence b sees all of the sequence's cached tokens, whatever the row's own position:
+ *   out[i][h][:] = sum_t softmax_t(scale * q[i][h] . K_b[t][h/G]) V_b[t][h/G],  0 <= t < context_lens[b],
+ *   row_starts[b] <= i < row_starts[b+1]
+ * Rows of one sequence may be the tokens of a prompt, one token, or the hypotheses of a beam.
+ * A context length of 0 gives zero rows.
+ *   q, out [device]: [total_rows][num_q_heads][head_dim], both of q_dtype (PKV_F16 or PKV_BF16;
+ *        for 16-bit pools the pool dtype), 16-byte aligned.  Sums and softmax are fp32, rounded once.
+ *   row_starts [device]: int32 [num_seqs + 1], ascending, in [0, total_rows].  A sequence may have
+ *        no rows; rows of no sequence (behind the last) are padding, their output is left as it is.
+ *   block_tables, context_lens [device]: as paged_decode_attn.
+ *   max_rows, max_context_len [host]: bounds of a sequence's rows and of context_lens.
+ *   workspace [device]: paged_cross_workspace_bytes(...) bytes, 16-byte aligned.
+ * All pool dtypes, head dims and group sizes.  On the device: lengths and row_starts out of range
+ * are clipped to the bounds and set PKV_DEV_BAD_LENGTH (rows past max_rows are not written).
+ */
+PKV_API int paged_cross_attn(pkv_pool_t pool, int layer, const void* q, int q_dtype, const int32_t* row_starts,
+                             int total_rows, int num_q_heads, const int32_t* block_tables, int block_table_width,
+                             const int32_t* context_lens, int num_seqs, int max_rows, int max_context_len, float scale,
+                             void* out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Workspace paged_prefill_chunk_attn needs (bytes). */
 PKV_API size_t paged_prefill_workspace_bytes(pkv_pool_t pool, int chunk_len, int num_q_heads, int ctx_before);
 

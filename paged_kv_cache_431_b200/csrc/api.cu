@@ -626,6 +626,190 @@ int paged_decode_attn_cascade(pkv_pool_t pool, int layer, const void* q, int q_d
     return launch_decode(a, tmk, tmv, s);
 }
 
+// ---- ragged batches: cross attention, decode over groups with prefixes ----------------
+
+// How a ragged launch splits the keys: tokens per partition and the partitions of the longest item.
+struct RaggedSplit {
+    int part, parts;
+};
+
+static RaggedSplit ragged_split(pkv_pool_t pool, int items, int max_rows, int G, int max_tokens)
+{
+    RaggedSplit r;
+    const int ctas = pool->d.num_kv_heads * ((max_rows * G + 15) / 16);
+    r.part = choose_partition(items, ctas, max_tokens, pool->row_bytes, is_quantized(pool->d.kv_dtype), nullptr);
+    r.parts = max_tokens > 0 ? (max_tokens + r.part - 1) / r.part : 1;
+    return r;
+}
+
+static size_t ragged_ws_bytes(pkv_pool_t pool, int rows, int num_q_heads, int slots)
+{
+    return (size_t)rows * num_q_heads * slots * (pool->d.head_dim + 2) * sizeof(float);
+}
+
+// The checks that both ragged calls share.  PKV_OK with *empty set: nothing to do.
+static int ragged_checks(pkv_pool_t pool, int layer, const void* q, int q_dtype, const void* out, int total_rows,
+                         int num_q_heads, int items, int max_rows, int block_table_width)
+{
+    const pkv_pool_desc& d = pool->d;
+    if (layer < 0 || layer >= d.num_layers || total_rows < 0 || num_q_heads <= 0 || items < 0 || max_rows < 0 ||
+        block_table_width <= 0)
+        return PKV_ERR_ARG;
+    if (num_q_heads % d.num_kv_heads) return PKV_ERR_SHAPE;
+    const int G = num_q_heads / d.num_kv_heads;
+    if (q_dtype != PKV_F16 && q_dtype != PKV_BF16) return PKV_ERR_DTYPE;
+    if (!is_quantized(d.kv_dtype) && q_dtype != d.kv_dtype) return PKV_ERR_DTYPE;
+    // grid limits: items in z, (KV head, 16 rows) in y, merge CTAs in x
+    if (items > 65535 || (long long)block_table_width * PKV_BLOCK_SIZE > 0x7fffffffLL ||
+        (long long)d.num_kv_heads * (((long long)max_rows * G + 15) / 16) > 65535 ||
+        (long long)total_rows * num_q_heads > 0x7fffffffLL)
+        return PKV_ERR_UNSUPPORTED;
+    if (items > 0 && max_rows > 0 && total_rows > 0) {
+        if (!q || !out) return PKV_ERR_NULL;
+        if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) return PKV_ERR_ARG;
+    }
+    return PKV_OK;
+}
+
+static RaggedArgs ragged_args(pkv_pool_t pool, int layer, const void* q, int q_dtype, int num_q_heads, float scale,
+                              int total_rows, const int32_t* tables, int W, const int32_t* ctx_lens,
+                              const int32_t* row_starts, void* out)
+{
+    const pkv_pool_desc& d = pool->d;
+    RaggedArgs a = {};
+    a.q = q;
+    a.q_dtype = q_dtype;
+    a.tables = tables;
+    a.W = W;
+    a.ctx_lens = ctx_lens;
+    a.row_starts = row_starts;
+    a.total_rows = total_rows;
+    a.H_q = num_q_heads;
+    a.H_kv = d.num_kv_heads;
+    a.G = num_q_heads / d.num_kv_heads;
+    a.N = d.num_blocks;
+    a.d = d.head_dim;
+    a.kv_dtype = d.kv_dtype;
+    a.scale = scale;
+    a.k_scale = pool->ks_base[layer];
+    a.v_scale = pool->vs_base[layer];
+    a.out = out;
+    a.status = d.device_status;
+    return a;
+}
+
+size_t paged_cross_workspace_bytes(pkv_pool_t pool, int total_rows, int num_q_heads, int num_seqs, int max_rows,
+                                   int max_context_len)
+{
+    if (!pool || total_rows < 0 || num_q_heads <= 0 || num_q_heads % pool->d.num_kv_heads || num_seqs < 0 ||
+        max_rows < 0 || max_context_len < 0)
+        return 0;
+    const RaggedSplit sp = ragged_split(pool, num_seqs, max_rows, num_q_heads / pool->d.num_kv_heads, max_context_len);
+    return sp.parts > 1 ? ragged_ws_bytes(pool, total_rows, num_q_heads, sp.parts) : 0;
+}
+
+int paged_cross_attn(pkv_pool_t pool, int layer, const void* q, int q_dtype, const int32_t* row_starts, int total_rows,
+                     int num_q_heads, const int32_t* block_tables, int block_table_width, const int32_t* context_lens,
+                     int num_seqs, int max_rows, int max_context_len, float scale, void* out, void* workspace,
+                     size_t workspace_bytes, void* stream)
+{
+    if (!pool) return PKV_ERR_NULL;
+    int rc = ragged_checks(pool, layer, q, q_dtype, out, total_rows, num_q_heads, num_seqs, max_rows, block_table_width);
+    if (rc != PKV_OK) return rc;
+    if (max_context_len < 0) return PKV_ERR_ARG;
+    if (num_seqs == 0 || total_rows == 0 || max_rows == 0) return PKV_OK;
+    if (!row_starts || !block_tables || !context_lens) return PKV_ERR_NULL;
+    RaggedArgs a = ragged_args(pool, layer, q, q_dtype, num_q_heads, scale, total_rows, block_tables,
+                               block_table_width, context_lens, row_starts, out);
+    const RaggedSplit sp = ragged_split(pool, num_seqs, max_rows, a.G, max_context_len);
+    const size_t need = sp.parts > 1 ? ragged_ws_bytes(pool, total_rows, num_q_heads, sp.parts) : 0;
+    if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15)))
+        return PKV_ERR_WORKSPACE;
+    const CUtensorMap *tmk = nullptr, *tmv = nullptr;
+    rc = layer_maps(pool, layer, &tmk, &tmv);
+    if (rc != PKV_OK) return rc;
+    a.mode = 0;   // kCross
+    a.items = a.starts = num_seqs;
+    a.max_rows = max_rows;
+    a.part_tokens = sp.part;
+    a.max_parts = a.slots = sp.parts;
+    a.ws_o = need ? static_cast<float*>(workspace) : nullptr;
+    a.ws_ml = need ? a.ws_o + (size_t)total_rows * num_q_heads * sp.parts * a.d : nullptr;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    rc = launch_ragged_short(a, tmk, tmv, s);
+    if (rc != PKV_OK || sp.parts <= 1) return rc;
+    return launch_ragged_merge(a, s);
+}
+
+size_t paged_decode_groups_workspace_bytes(pkv_pool_t pool, int num_seqs, int num_q_heads, int num_groups,
+                                           int max_group_size, int max_prefix_len, int max_suffix_len)
+{
+    if (!pool || num_seqs < 0 || num_q_heads <= 0 || num_q_heads % pool->d.num_kv_heads || num_groups < 0 ||
+        max_group_size < 0 || max_prefix_len < 0 || max_suffix_len < 0)
+        return 0;
+    const int G = num_q_heads / pool->d.num_kv_heads;
+    const int pre = max_prefix_len > 0 ? ragged_split(pool, num_groups, max_group_size, G, max_prefix_len).parts : 0;
+    const int own = ragged_split(pool, num_seqs, 1, G, max_suffix_len).parts;
+    return pre + own > 1 ? ragged_ws_bytes(pool, num_seqs, num_q_heads, pre + own) : 0;
+}
+
+int paged_decode_attn_groups(pkv_pool_t pool, int layer, const void* q, int q_dtype, const int32_t* block_tables,
+                             int block_table_width, const int32_t* context_lens, int num_seqs, int num_q_heads,
+                             const int32_t* group_starts, const int32_t* prefix_lens, int num_groups,
+                             int max_group_size, int max_prefix_len, int max_suffix_len, float scale, void* out,
+                             void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (!pool) return PKV_ERR_NULL;
+    int rc = ragged_checks(pool, layer, q, q_dtype, out, num_seqs, num_q_heads, num_groups, max_group_size,
+                           block_table_width);
+    if (rc != PKV_OK) return rc;
+    if (max_prefix_len < 0 || max_suffix_len < 0 || (long long)max_prefix_len + max_suffix_len > 0x7fffffffLL)
+        return PKV_ERR_ARG;
+    if (num_seqs > 65535) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || num_groups == 0 || max_group_size == 0) return PKV_OK;
+    if (!block_tables || !context_lens || !group_starts || !prefix_lens) return PKV_ERR_NULL;
+    RaggedArgs a = ragged_args(pool, layer, q, q_dtype, num_q_heads, scale, num_seqs, block_tables, block_table_width,
+                               context_lens, group_starts, out);
+    const RaggedSplit pre = max_prefix_len > 0 ? ragged_split(pool, num_groups, max_group_size, a.G, max_prefix_len)
+                                               : RaggedSplit{PKV_BLOCK_SIZE, 0};
+    const RaggedSplit own = ragged_split(pool, num_seqs, 1, a.G, max_suffix_len);
+    const int slots = pre.parts + own.parts;
+    const size_t need = slots > 1 ? ragged_ws_bytes(pool, num_seqs, num_q_heads, slots) : 0;
+    if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15)))
+        return PKV_ERR_WORKSPACE;
+    const CUtensorMap *tmk = nullptr, *tmv = nullptr;
+    rc = layer_maps(pool, layer, &tmk, &tmv);
+    if (rc != PKV_OK) return rc;
+    a.starts = num_groups;
+    a.prefix_lens = prefix_lens;
+    a.max_prefix = max_prefix_len;
+    a.slots = slots;
+    a.ws_o = need ? static_cast<float*>(workspace) : nullptr;
+    a.ws_ml = need ? a.ws_o + (size_t)num_seqs * num_q_heads * slots * a.d : nullptr;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // 1. every group's prefix, once for the group's rows
+    if (pre.parts > 0) {
+        a.mode = 1;   // kPrefix
+        a.items = num_groups;
+        a.max_rows = max_group_size;
+        a.part_tokens = pre.part;
+        a.max_parts = pre.parts;
+        rc = launch_ragged_short(a, tmk, tmv, s);
+        if (rc != PKV_OK) return rc;
+    }
+    // 2. every sequence's own tokens, 3. the merge of both
+    a.mode = 2;   // kSuffix
+    a.items = num_seqs;
+    a.max_rows = 1;
+    a.part_tokens = own.part;
+    a.max_parts = own.parts;
+    a.part_base = pre.parts;
+    a.pre_part = pre.part;
+    rc = launch_ragged_short(a, tmk, tmv, s);
+    if (rc != PKV_OK || slots <= 1) return rc;
+    return launch_ragged_merge(a, s);
+}
+
 size_t paged_prefill_workspace_bytes(pkv_pool_t pool, int chunk_len, int num_q_heads, int ctx_before)
 {
     (void)pool;

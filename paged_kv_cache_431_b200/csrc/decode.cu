@@ -53,8 +53,9 @@ struct Mma16Cfg {
 // NW = 1: one warp per (partition, KV head or group of 16 of its query heads, sequence).
 // NW > 1 (groups of 17..64 query heads): NW warps share one K/V ring, warp w taking query
 // heads 16w .. 16w+15 of the group, so every K/V tile crosses into the SM once; a stage is
-// refilled once all warps have released it.
-template <int D, bool BF16, int NHT, int STAGES, int NW>
+// refilled once all warps have released it.  RAG: the ragged form, where the rows of a group of
+// 16 are (query row, head) pairs of one item and the output is 16-bit.
+template <int D, bool BF16, int NHT, int STAGES, int NW, bool RAG>
 __global__ void __launch_bounds__(32 * NW)
 decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV)
@@ -70,25 +71,48 @@ decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
     const int part = blockIdx.x, b = blockIdx.z;
     const int g = NW > 1 ? blockIdx.y : blockIdx.y / p.hgroups;               // KV head
     const int hg = NW > 1 ? warp : blockIdx.y - g * p.hgroups;                // group of 16 query heads
-    const int GC = min(16, p.G - 16 * hg);                                   // query heads of this warp
     const int r = lane >> 2, qd = lane & 3;
     const int hbase = g * p.G + 16 * hg;
-
-    const int ctx = checked_ctx(p, b, threadIdx.x == 0 && part == 0 && g == 0);
-    const int nparts = part_count(p, ctx);
-    const int tok0 = seq_base(p, ctx) + part * p.part_tokens;
-    const int lo = visible_lo(p, ctx);   // tokens before lo are outside the window
-    if (tok0 >= ctx) {
-        if (part == 0 && p.part_base == 0) {   // empty context: a zero row
-            float* o = p.out + ((size_t)b * p.H_q + hbase) * D;
-            for (int i = lane; i < GC * D; i += 32) o[i] = 0.f;
+    int GC, ctx, nparts, tok0, lo;
+    RaggedItem it;
+    const int32_t* trow;
+    if constexpr (RAG) {
+        it = ragged_item(p.rg, p.ctx_lens, p.W, p.max_parts * p.part_tokens, b, p.status,
+                         threadIdx.x == 0 && part == 0 && blockIdx.y == 0);
+        GC = min(16, it.rows * p.G - 16 * hg);   // query rows of this warp; none: it only helps
+        ctx = it.end;
+        nparts = (ctx - it.base + p.part_tokens - 1) / p.part_tokens;
+        tok0 = it.base + part * p.part_tokens;
+        lo = 0;
+        if (it.rows * p.G <= (NW > 1 ? 0 : 16 * hg)) return;
+        if (tok0 >= ctx) {
+            if (part == 0 && it.whole) {   // no keys at all: zero rows
+                for (int i = lane; i < GC * (D / 4); i += 32)
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.rg.out16) +
+                                              ragged_row(it, p.G, p.H_q, g, 16 * hg + i / (D / 4)) * D +
+                                              4 * (i % (D / 4))) = make_uint2(0u, 0u);
+            }
+            return;
         }
-        return;
+        trow = p.tables + (size_t)it.table * p.W + tok0 / kBlock;
+    } else {
+        GC = min(16, p.G - 16 * hg);             // query heads of this warp
+        ctx = checked_ctx(p, b, threadIdx.x == 0 && part == 0 && g == 0);
+        nparts = part_count(p, ctx);
+        tok0 = seq_base(p, ctx) + part * p.part_tokens;
+        lo = visible_lo(p, ctx);   // tokens before lo are outside the window
+        if (tok0 >= ctx) {
+            if (part == 0 && p.part_base == 0) {   // empty context: a zero row
+                float* o = p.out + ((size_t)b * p.H_q + hbase) * D;
+                for (int i = lane; i < GC * D; i += 32) o[i] = 0.f;
+            }
+            return;
+        }
+        trow = p.tables + (size_t)b * p.W + tok0 / kBlock;
     }
     const int ntok = min(p.part_tokens, ctx - tok0);
     const int ntiles = (ntok + kBlock - 1) / kBlock;
 
-    const int32_t* trow = p.tables + (size_t)b * p.W + tok0 / kBlock;
     for (int j = threadIdx.x; j < ntiles; j += 32 * NW) {
         int blk = trow[j];
         if ((unsigned)blk >= (unsigned)p.N) {
@@ -136,15 +160,28 @@ decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
     // Q as the A operand of S = Q.K^T: rows = heads (r and r + 8), 16 dims per k-step.
     uint32_t qa[D / 16][4];
     {
+        const bool r0 = r < GC, r1 = (NHT == 2) && (r + 8 < GC);
+        if constexpr (RAG) {
+            const uint32_t* q32 = static_cast<const uint32_t*>(p.q);
+            const uint32_t* qr0 = q32 + (r0 ? ragged_row(it, p.G, p.H_q, g, 16 * hg + r) * (D / 2) : 0);
+            const uint32_t* qr1 = q32 + (r1 ? ragged_row(it, p.G, p.H_q, g, 16 * hg + r + 8) * (D / 2) : 0);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                qa[ks][0] = r0 ? __ldg(qr0 + 8 * ks + qd) : 0u;
+                qa[ks][2] = r0 ? __ldg(qr0 + 8 * ks + 4 + qd) : 0u;
+                qa[ks][1] = r1 ? __ldg(qr1 + 8 * ks + qd) : 0u;
+                qa[ks][3] = r1 ? __ldg(qr1 + 8 * ks + 4 + qd) : 0u;
+            }
+        } else {
         const uint32_t* q32 = reinterpret_cast<const uint32_t*>(
             static_cast<const uint16_t*>(p.q) + ((size_t)b * p.H_q + hbase) * D);
-        const bool r0 = r < GC, r1 = (NHT == 2) && (r + 8 < GC);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
             qa[ks][0] = r0 ? __ldg(q32 + (r * D + 16 * ks + 2 * qd) / 2) : 0u;
             qa[ks][2] = r0 ? __ldg(q32 + (r * D + 16 * ks + 8 + 2 * qd) / 2) : 0u;
             qa[ks][1] = r1 ? __ldg(q32 + ((r + 8) * D + 16 * ks + 2 * qd) / 2) : 0u;
             qa[ks][3] = r1 ? __ldg(q32 + ((r + 8) * D + 16 * ks + 8 + 2 * qd) / 2) : 0u;
+        }
         }
     }
 
@@ -309,7 +346,7 @@ decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
     // ---- epilogue: O rows [head][dim] through shared memory, then coalesced stores
 #pragma unroll
     for (int hr = 0; hr < NHT; ++hr) l_run[hr] = warp_sum_quad(l_run[hr]);
-    const bool final_out = (p.part_base == 0 && nparts == 1);
+    const bool final_out = RAG ? (it.whole && nparts == 1) : (p.part_base == 0 && nparts == 1);
     float* so = reinterpret_cast<float*>(smem) + warp * 16 * (D + 4);
     constexpr int SR = D + 4;   // padded row stride (floats)
     __syncwarp();
@@ -333,7 +370,26 @@ decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
     }
     __syncwarp();
     const size_t row0 = (size_t)b * p.H_q + hbase;
-    if (final_out) {
+    if constexpr (RAG) {
+        // final rows rounded once to q's dtype; partials as in the plain form, by query row
+        for (int i = lane; i < GC * (D / 4); i += 32) {
+            const int h = i / (D / 4), c4 = i % (D / 4);
+            const float4 v = *reinterpret_cast<const float4*>(&so[h * SR + 4 * c4]);
+            const size_t row = ragged_row(it, p.G, p.H_q, g, 16 * hg + h);
+            if (final_out)
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.rg.out16) + row * D + 4 * c4) = pack4(v, BF16);
+            else
+                st_hint(reinterpret_cast<float4*>(p.ws_o + ws_slot(p, row, part) * D + 4 * c4), v, l2_evict_last());
+        }
+        if (!final_out && qd == 0) {
+#pragma unroll
+            for (int hr = 0; hr < NHT; ++hr)
+                if (r + 8 * hr < GC)
+                    st_hint(reinterpret_cast<float2*>(
+                                p.ws_ml + ws_slot(p, ragged_row(it, p.G, p.H_q, g, 16 * hg + r + 8 * hr), part) * 2),
+                            make_float2(m_run[hr], l_run[hr]), l2_evict_last());
+        }
+    } else if (final_out) {
         for (int i = lane; i < GC * (D / 4); i += 32) {
             const int h = i / (D / 4), c4 = i % (D / 4);
             const float4 v = *reinterpret_cast<const float4*>(&so[h * SR + 4 * c4]);
@@ -447,6 +503,102 @@ __global__ void __launch_bounds__(32 * kMergeHeads) decode_reduce_kernel(const D
     }
 }
 
+// The merge of the ragged form: row t of q belongs to one item; a row that one partition covered
+// whole was written by it, a row of no item is left as it is.  In a grouped batch the prefix's
+// partials (slots 0 ..) come before the suffix's (slots pre_slots ..).
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeHeads) ragged_merge_kernel(const DecodeParams p)
+{
+    const int lane = threadIdx.x & 31;
+    const int per_row = (p.H_q + kMergeHeads - 1) / kMergeHeads;
+    const int t = blockIdx.x / per_row;
+    const int h = (blockIdx.x % per_row) * kMergeHeads + (threadIdx.x >> 5);
+    const RaggedParams& r = p.rg;
+    const int item = item_of_row(r, t);
+    if (item < 0 || h >= p.H_q) return;
+    int pre = 0, own;      // partials of the prefix, of the rest
+    bool whole = true;
+    if (r.mode == kSuffix) {
+        const RaggedItem it = ragged_item(r, p.ctx_lens, p.W, p.max_parts * p.part_tokens, t, p.status, false);
+        pre = (it.base + r.pre_part - 1) / r.pre_part;
+        own = (it.end - it.base + p.part_tokens - 1) / p.part_tokens;
+        whole = it.whole;
+        if (h == 0) {      // the table must start with its group's prefix
+            const int32_t* mine = p.tables + (size_t)t * p.W;
+            const int32_t* first = p.tables + (size_t)max(0, r.row_starts[item]) * p.W;
+            bool same = true;
+            for (int j = lane; j < it.base / kBlock; j += 32) same &= mine[j] == first[j];
+            if (!__all_sync(0xffffffffu, same) && lane == 0) flag_status(p.status, PKV_DEV_BAD_PREFIX);
+        }
+    } else {
+        int row0, rows;
+        item_rows(r, item, row0, rows, p.status, false);
+        if (t >= row0 + rows) return;            // beyond what the grid covered
+        const RaggedItem it = ragged_item(r, p.ctx_lens, p.W, p.max_parts * p.part_tokens, item, p.status, false);
+        own = (it.end + p.part_tokens - 1) / p.part_tokens;
+    }
+    pdl_wait_primary();   // the partials of the kernels before this one
+    const int n = pre + own;
+    if (whole && n <= 1) return;
+    const size_t row = (size_t)t * p.H_q + h;
+    const size_t base = row * p.slots;
+    const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + base;
+    constexpr int V = D / 32;   // floats per lane
+    constexpr int kBatch = 8;   // partial rows loaded together
+    const float* po = p.ws_o + base * D + lane * V;
+    auto slot = [&](int i) { return i < pre ? i : p.part_base + i - pre; };
+
+    float M = -INFINITY, L = 0.f;
+    float acc[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+    for (int i0 = 0; i0 < n; i0 += kBatch) {
+        const int nb = min(kBatch, n - i0);
+        const float2 mlk = lane < nb ? ml[slot(i0 + lane)] : make_float2(-INFINITY, 0.f);
+        float v[kBatch][V];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[k][e] = 0.f;
+            if (k < nb) {
+                const float* src = po + (size_t)slot(i0 + k) * D;
+                if constexpr (V == 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(src);
+                    v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2*>(src);
+                    v[k][0] = x.x; v[k][1] = x.y;
+                }
+            }
+        }
+        float mb = mlk.x;
+#pragma unroll
+        for (int off = 4; off; off >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, off));
+        mb = __shfl_sync(0xffffffffu, mb, 0);
+        const float Mn = fmaxf(M, mb);
+        const float ref = Mn == -INFINITY ? 0.f : Mn;
+        const float a = ex2(M - ref);
+        float lb = lane < nb ? ex2(mlk.x - ref) * mlk.y : 0.f;
+#pragma unroll
+        for (int off = 4; off; off >>= 1) lb += __shfl_xor_sync(0xffffffffu, lb, off);
+        L = L * a + __shfl_sync(0xffffffffu, lb, 0);
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] *= a;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const float w = k < nb ? ex2(__shfl_sync(0xffffffffu, mlk.x, k) - ref) : 0.f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] += w * v[k][e];
+        }
+        M = Mn;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(r.out16) + row * D + lane * V);
+#pragma unroll
+    for (int e = 0; e < V; e += 2)
+        out[e / 2] = p.q_bf16 ? pack2<true>(acc[e] * inv, acc[e + 1] * inv) : pack2<false>(acc[e] * inv, acc[e + 1] * inv);
+}
+
 // ---------------------------------------------------------------------------
 // launcher
 // ---------------------------------------------------------------------------
@@ -489,28 +641,28 @@ int launch_k(K kernel, int smem, dim3 grid, int threads, cudaStream_t s, const D
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
-template <int D, bool BF16, int NW>
+template <int D, bool BF16, int NW, bool RAG>
 int launch_mma16_nw(const DecodeParams& p, int nht, dim3 grid, cudaStream_t s, const CUtensorMap* tmk,
                     const CUtensorMap* tmv)
 {
     constexpr int smem = Mma16Cfg<D, kStages, NW>::SMEM;
     if (nht == 1)
-        return launch_k(decode_mma16_kernel<D, BF16, 1, kStages, NW>, smem, grid, 32 * NW, s, p, tmk, tmv);
-    return launch_k(decode_mma16_kernel<D, BF16, 2, kStages, NW>, smem, grid, 32 * NW, s, p, tmk, tmv);
+        return launch_k(decode_mma16_kernel<D, BF16, 1, kStages, NW, RAG>, smem, grid, 32 * NW, s, p, tmk, tmv);
+    return launch_k(decode_mma16_kernel<D, BF16, 2, kStages, NW, RAG>, smem, grid, 32 * NW, s, p, tmk, tmv);
 }
 
 // Groups of 17..64 query heads run as one CTA of ceil(G / 16) warps sharing the K/V ring;
 // wider groups as one single-warp CTA per 16 heads.
-template <int D, bool BF16>
+template <int D, bool BF16, bool RAG = false>
 int launch_mma16(const DecodeParams& p, int nht, dim3 grid, cudaStream_t s, const CUtensorMap* tmk,
                  const CUtensorMap* tmv)
 {
     const dim3 g1(grid.x, grid.y / p.hgroups, grid.z);   // one CTA per KV head
     switch (p.hgroups) {
-    case 2: return launch_mma16_nw<D, BF16, 2>(p, nht, g1, s, tmk, tmv);
-    case 3: return launch_mma16_nw<D, BF16, 3>(p, nht, g1, s, tmk, tmv);
-    case 4: return launch_mma16_nw<D, BF16, 4>(p, nht, g1, s, tmk, tmv);
-    default: return launch_mma16_nw<D, BF16, 1>(p, nht, grid, s, tmk, tmv);
+    case 2: return launch_mma16_nw<D, BF16, 2, RAG>(p, nht, g1, s, tmk, tmv);
+    case 3: return launch_mma16_nw<D, BF16, 3, RAG>(p, nht, g1, s, tmk, tmv);
+    case 4: return launch_mma16_nw<D, BF16, 4, RAG>(p, nht, g1, s, tmk, tmv);
+    default: return launch_mma16_nw<D, BF16, 1, RAG>(p, nht, grid, s, tmk, tmv);
     }
 }
 
@@ -603,6 +755,76 @@ int launch_decode(const DecodeArgs& a, const CUtensorMap* tmk, const CUtensorMap
         if (e != cudaSuccess) return PKV_ERR_CUDA;
     }
     return PKV_OK;
+}
+
+static DecodeParams ragged_params(const RaggedArgs& a)
+{
+    DecodeParams p = {};
+    p.q = a.q;
+    p.tables = a.tables;
+    p.ctx_lens = a.ctx_lens;
+    p.k_scale = a.k_scale;
+    p.v_scale = a.v_scale;
+    p.ws_o = a.ws_o;
+    p.ws_ml = a.ws_ml;
+    p.status = a.status;
+    p.W = a.W;
+    p.H_q = a.H_q;
+    p.H_kv = a.H_kv;
+    p.G = a.G;
+    p.N = a.N;
+    p.part_tokens = a.part_tokens;
+    p.max_parts = a.max_parts;
+    p.num_seqs = a.items;
+    p.part_base = a.part_base;
+    p.slots = a.slots;
+    p.hgroups = (a.max_rows * a.G + 15) / 16;
+    p.q_bf16 = a.q_dtype == PKV_BF16;
+    p.scale_log2 = a.scale * kLog2e;
+    const WaitHook hook = wait_hook();
+    p.hold_tile = hook.hold_tile;
+    p.wait_cycles = hook.wait_cycles;
+    p.rg.mode = a.mode;
+    p.rg.row_starts = a.row_starts;
+    p.rg.prefix_lens = a.prefix_lens;
+    p.rg.items = a.starts;
+    p.rg.total_rows = a.total_rows;
+    p.rg.max_rows = a.max_rows;
+    p.rg.max_prefix = a.max_prefix;
+    p.rg.pre_part = a.pre_part;
+    p.rg.pre_slots = a.part_base;
+    p.rg.out16 = a.out;
+    return p;
+}
+
+int launch_ragged_short(const RaggedArgs& a, const CUtensorMap* tmk, const CUtensorMap* tmv, cudaStream_t s)
+{
+    const DecodeParams p = ragged_params(a);
+    const dim3 grid(a.max_parts, a.H_kv * p.hgroups, a.items);
+    const int nht = a.max_rows * a.G <= 8 ? 1 : 2;
+    if (is_quantized(a.kv_dtype)) return launch_decode_quant_ragged(p, a.kv_dtype, a.d, nht, grid, s, tmk, tmv);
+    const bool bf = a.kv_dtype == PKV_BF16;
+    if (a.d == 128) return bf ? launch_mma16<128, true, true>(p, nht, grid, s, tmk, tmv)
+                              : launch_mma16<128, false, true>(p, nht, grid, s, tmk, tmv);
+    return bf ? launch_mma16<64, true, true>(p, nht, grid, s, tmk, tmv)
+              : launch_mma16<64, false, true>(p, nht, grid, s, tmk, tmv);
+}
+
+int launch_ragged_merge(const RaggedArgs& a, cudaStream_t s)
+{
+    const DecodeParams p = ragged_params(a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.H_q + kMergeHeads - 1) / kMergeHeads) * a.total_rows);
+    cfg.blockDim = dim3(32 * kMergeHeads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = a.d == 128 ? cudaLaunchKernelEx(&cfg, ragged_merge_kernel<128>, p)
+                                     : cudaLaunchKernelEx(&cfg, ragged_merge_kernel<64>, p);
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // namespace pkv

@@ -17,6 +17,28 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr bool kHintKV = (PKV_L2_HINTS & 1) != 0;
 constexpr bool kHintPartials = (PKV_L2_HINTS & 2) != 0;
 
+// Ragged form (paged_cross_attn, paged_decode_attn_groups): a grid z index is an item, a run of
+// query rows that share their keys.
+//   kCross   item = sequence b: rows row_starts[b] .. row_starts[b+1]-1 against its own cached
+//            tokens 0 .. ctx_lens[b]-1
+//   kPrefix  item = group g: rows (sequences) row_starts[g] .. against the group's prefix, by
+//            the table of its first sequence
+//   kSuffix  item = sequence b of the grouped batch: its one row against the tokens from its
+//            group's prefix to its context's end
+// A KV head's query rows of an item are (row, head of the group), row major.
+enum RaggedMode { kCross = 0, kPrefix = 1, kSuffix = 2 };
+
+struct RaggedParams {
+    int mode;
+    const int32_t* row_starts;    // [items + 1]; kSuffix: [groups + 1]
+    const int32_t* prefix_lens;   // [groups] (kPrefix, kSuffix)
+    int items;                    // row_starts has items + 1 entries
+    int total_rows, max_rows;     // rows of q; rows of an item that the grid covers
+    int max_prefix;               // kPrefix, kSuffix: tokens of a prefix that the grid covers
+    int pre_part, pre_slots;      // kSuffix and its merge: tokens per prefix partition, workspace slots before the suffix's
+    void* out16;                  // [total_rows][H_q][d] of q's dtype
+};
+
 struct DecodeParams {
     const void* q;
     const int32_t* tables;
@@ -41,6 +63,7 @@ struct DecodeParams {
     float scale_log2;
     int hold_tile;          // test hook: this CTA-local tile's copy is never issued (-1: none)
     long long wait_cycles;  // bound of every wait on a copy (SM cycles)
+    RaggedParams rg;        // ragged form only
 };
 
 // Context length of sequence b, clamped to what the table and the grid can cover (with a
@@ -80,6 +103,92 @@ __device__ __forceinline__ size_t ws_slot(const DecodeParams& p, size_t row, int
     return row * p.slots + p.part_base + part;
 }
 
+// An item of the ragged form: query rows row0 .. row0 + rows - 1 against tokens base .. end-1 of
+// the sequence whose table is row `table`; `whole` when no other keys belong to these rows.
+struct RaggedItem {
+    int row0, rows, table, base, end;
+    bool whole;
+};
+
+// Tokens of group g's prefix: whole blocks, within the table and the grid.
+__device__ __forceinline__ int group_prefix(const RaggedParams& r, int W, int g, int32_t* status, bool report)
+{
+    int n = r.prefix_lens[g];
+    const int cap = min(W * kBlock, r.max_prefix);
+    if (n < 0 || n > cap) {
+        if (report) flag_status(status, PKV_DEV_BAD_LENGTH);
+        n = n < 0 ? 0 : cap;
+    }
+    if (n % kBlock) {
+        if (report) flag_status(status, PKV_DEV_BAD_PREFIX);
+        n -= n % kBlock;
+    }
+    return n;
+}
+
+// Rows of item i, clipped to q's rows and to what the grid covers (`report` flags a clip).
+__device__ __forceinline__ void item_rows(const RaggedParams& r, int i, int& row0, int& rows, int32_t* status, bool report)
+{
+    const int a = r.row_starts[i], b = r.row_starts[i + 1];
+    row0 = max(0, min(a, r.total_rows));
+    rows = max(0, min(min(b, r.total_rows) - row0, r.max_rows));
+    if (report && (a != row0 || b < a || b - a != rows)) flag_status(status, PKV_DEV_BAD_LENGTH);
+}
+
+// The item whose rows hold row t, or -1 (one whole warp asks).  The 32 lanes look at 32 items at
+// a time, so that a batch of hundreds is a few independent loads.
+__device__ __forceinline__ int item_of_row(const RaggedParams& r, int t)
+{
+    const int lane = threadIdx.x & 31;
+    for (int i0 = 0; i0 < r.items; i0 += 32) {
+        const int i = i0 + lane;
+        const bool in = i < r.items && r.row_starts[i] <= t && t < r.row_starts[i + 1];
+        const unsigned hit = __ballot_sync(0xffffffffu, in);
+        if (hit) return i0 + __ffs(hit) - 1;
+    }
+    return -1;
+}
+
+// Item b of the launch (one whole warp asks).  rows 0: nothing to do.
+__device__ __forceinline__ RaggedItem ragged_item(const RaggedParams& r, const int32_t* ctx_lens, int W, int max_tokens,
+                                                  int b, int32_t* status, bool report)
+{
+    RaggedItem it;
+    it.base = 0;
+    if (r.mode == kSuffix) {
+        const int g = item_of_row(r, b);
+        it.row0 = it.table = b;
+        it.rows = g >= 0 ? 1 : 0;                // a sequence behind the last group is padding
+        it.end = g >= 0 ? ctx_lens[b] : 0;
+        it.base = g >= 0 ? group_prefix(r, W, g, status, report) : 0;
+        it.whole = it.base == 0;
+    } else {
+        item_rows(r, b, it.row0, it.rows, status, report);
+        it.whole = r.mode == kCross;
+        it.table = it.whole ? b : it.row0;
+        it.end = it.rows == 0 ? 0 : it.whole ? ctx_lens[b] : group_prefix(r, W, b, status, report);
+    }
+    const int cap = min(W * kBlock, it.base + max_tokens);
+    if (it.end < it.base || it.end > cap) {
+        if (report) flag_status(status, PKV_DEV_BAD_LENGTH);
+        it.end = it.end < it.base ? it.base : cap;
+    }
+    return it;
+}
+
+// Index (in rows of H_q heads, flattened) of the item's query row n of KV head g.
+__device__ __forceinline__ size_t ragged_row(const RaggedItem& it, int G, int H_q, int g, int n)
+{
+    return (size_t)(it.row0 + n / G) * H_q + g * G + n % G;
+}
+
+// Four floats as 16-bit values of q's dtype.
+__device__ __forceinline__ uint2 pack4(float4 v, bool bf16)
+{
+    return bf16 ? make_uint2(pack2<true>(v.x, v.y), pack2<true>(v.z, v.w))
+                : make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
+}
+
 // Byte address of 16-byte chunk `c` of row `t` in a tile stored as 128-byte-wide TMA
 // boxes of 16 rows with the 128-byte swizzle (chunk index XOR row % 8).
 __device__ __forceinline__ uint32_t swz128(uint32_t tile, int t, int c)
@@ -112,5 +221,8 @@ int launch_decode_tc_fp8(const DecodeParams& p, const CUtensorMap* tmk, const CU
 // Launch the quantized-pool decode kernel (decode_quant.cu).
 int launch_decode_quant(const DecodeParams& p, int kv_dtype, int d, int nht, dim3 grid, cudaStream_t s,
                         const CUtensorMap* tmk, const CUtensorMap* tmv);
+// The same kernels over ragged items (decode.cu, decode_quant.cu).
+int launch_decode_quant_ragged(const DecodeParams& p, int kv_dtype, int d, int nht, dim3 grid, cudaStream_t s,
+                               const CUtensorMap* tmk, const CUtensorMap* tmv);
 
 }  // namespace pkv

@@ -246,7 +246,8 @@ __device__ __forceinline__ void vfrags(uint32_t a, uint32_t b, uint32_t c, uint3
     }
 }
 
-template <int DT, int D, int NHT>
+// RAG: the ragged form (rows are (query row, head) pairs of one item, 16-bit output).
+template <int DT, int D, int NHT, bool RAG>
 __global__ void __launch_bounds__(32)
 decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV)
@@ -281,20 +282,44 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
     const int lane = threadIdx.x;
     const int part = blockIdx.x, b = blockIdx.z;
     const int g = blockIdx.y / p.hgroups, hg = blockIdx.y - g * p.hgroups;   // KV head, group of 16 heads
-    const int GC = min(16, p.G - 16 * hg);                                   // query heads of this CTA
     const int r = lane >> 2, qd = lane & 3;
     const int hbase = g * p.G + 16 * hg;
-
-    const int ctx = checked_ctx(p, b, lane == 0 && part == 0 && g == 0);
-    const int nparts = part_count(p, ctx);
-    const int tok0 = seq_base(p, ctx) + part * p.part_tokens;
-    const int lo = visible_lo(p, ctx);   // tokens before lo are outside the window
-    if (tok0 >= ctx) {
-        if (part == 0 && p.part_base == 0) {   // empty context: a zero row
-            float* o = p.out + ((size_t)b * p.H_q + hbase) * D;
-            for (int i = lane; i < GC * D; i += 32) o[i] = 0.f;
+    int GC, ctx, nparts, tok0, lo;
+    RaggedItem it;
+    const int32_t* trow;
+    if constexpr (RAG) {
+        it = ragged_item(p.rg, p.ctx_lens, p.W, p.max_parts * p.part_tokens, b, p.status,
+                         lane == 0 && part == 0 && blockIdx.y == 0);
+        GC = min(16, it.rows * p.G - 16 * hg);   // query rows of this CTA
+        ctx = it.end;
+        nparts = (ctx - it.base + p.part_tokens - 1) / p.part_tokens;
+        tok0 = it.base + part * p.part_tokens;
+        lo = 0;
+        if (GC <= 0) return;
+        if (tok0 >= ctx) {
+            if (part == 0 && it.whole) {   // no keys at all: zero rows
+                for (int i = lane; i < GC * (D / 4); i += 32)
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.rg.out16) +
+                                              ragged_row(it, p.G, p.H_q, g, 16 * hg + i / (D / 4)) * D +
+                                              4 * (i % (D / 4))) = make_uint2(0u, 0u);
+            }
+            return;
         }
-        return;
+        trow = p.tables + (size_t)it.table * p.W + tok0 / kBlock;
+    } else {
+        GC = min(16, p.G - 16 * hg);             // query heads of this CTA
+        ctx = checked_ctx(p, b, lane == 0 && part == 0 && g == 0);
+        nparts = part_count(p, ctx);
+        tok0 = seq_base(p, ctx) + part * p.part_tokens;
+        lo = visible_lo(p, ctx);   // tokens before lo are outside the window
+        if (tok0 >= ctx) {
+            if (part == 0 && p.part_base == 0) {   // empty context: a zero row
+                float* o = p.out + ((size_t)b * p.H_q + hbase) * D;
+                for (int i = lane; i < GC * D; i += 32) o[i] = 0.f;
+            }
+            return;
+        }
+        trow = p.tables + (size_t)b * p.W + tok0 / kBlock;
     }
     const int ntok = min(p.part_tokens, ctx - tok0);
     const int ntiles = (ntok + kBlock - 1) / kBlock;
@@ -304,7 +329,10 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
     float2* tsc = reinterpret_cast<float2*>(smem + Cfg::BODY);
     int* tbl = reinterpret_cast<int*>(tsc + p.part_tokens / kBlock);
-    const int32_t* trow = p.tables + (size_t)b * p.W + tok0 / kBlock;
+    // ragged form: the V scales of the partition times 2^ev, which brings the largest to [1, 2), so
+    // that P times a scale keeps fp16's range whatever the pool's magnitude (undone in the epilogue)
+    float v_unit = 1.f;
+    float vs_max = 0.f;
     for (int j = lane; j < ntiles; j += 32) {
         int blk = trow[j];
         if ((unsigned)blk >= (unsigned)p.N) {
@@ -314,6 +342,12 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
         tbl[j] = blk;
         const size_t si = (size_t)blk * p.H_kv + g;
         tsc[j] = make_float2(p.k_scale[si], p.v_scale[si]);
+        if constexpr (RAG) vs_max = fmaxf(vs_max, tsc[j].y);
+    }
+    if constexpr (RAG) {
+        const int ev = pow2_shift(warp_max(vs_max)) - 13;
+        for (int j = lane; j < ntiles; j += 32) tsc[j].y *= pow2f(ev);
+        v_unit = pow2f(-ev);
     }
     if (lane == 0) {
         for (int s = 0; s < STAGES; ++s) mbar_init(smem_u32(&bars[s]), 1);
@@ -358,7 +392,12 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
         const bool bf = p.q_bf16;
         const uint16_t* qh = static_cast<const uint16_t*>(p.q) + ((size_t)b * p.H_q + hbase) * D;
         auto qv = [&](int row, int dim) -> float {
-            const uint16_t u = __ldg(qh + row * D + dim);
+            uint16_t u;
+            if constexpr (RAG)
+                u = __ldg(static_cast<const uint16_t*>(p.q) +
+                          ragged_row(it, p.G, p.H_q, g, 16 * hg + row + dim / D) * D + dim % D);
+            else
+                u = __ldg(qh + row * D + dim);
             return bf ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
         };
         const bool r0 = r < GC, r1 = (NHT == 2) && (r + 8 < GC);
@@ -608,7 +647,7 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
     // ---- epilogue: O^T row (D/8) r + 2 mt (+1 for the second half) -> [head][dim]
 #pragma unroll
     for (int hr = 0; hr < NHT; ++hr) l_run[hr] = warp_sum_quad(l_run[hr]);
-    const bool final_out = (p.part_base == 0 && nparts == 1);
+    const bool final_out = RAG ? (it.whole && nparts == 1) : (p.part_base == 0 && nparts == 1);
     float* so = reinterpret_cast<float*>(smem);
     constexpr int SR = D + 4;
     __syncwarp();
@@ -621,6 +660,10 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
             inv_lo = 1.f / la;
             inv_hi = 1.f / lb;
         }
+        if constexpr (RAG) {
+            inv_lo *= v_unit;
+            inv_hi *= v_unit;
+        }
         const int h0 = 8 * hn + 2 * qd;
 #pragma unroll
         for (int mt = 0; mt < Cfg::MT; ++mt) {
@@ -632,6 +675,26 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
         }
     }
     __syncwarp();
+    if constexpr (RAG) {   // final rows rounded once to q's dtype; partials by query row
+        for (int i = lane; i < GC * (D / 4); i += 32) {
+            const int h = i / (D / 4), c4 = i % (D / 4);
+            const float4 v = *reinterpret_cast<const float4*>(&so[h * SR + 4 * c4]);
+            const size_t row = ragged_row(it, p.G, p.H_q, g, 16 * hg + h);
+            if (final_out)
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.rg.out16) + row * D + 4 * c4) = pack4(v, p.q_bf16);
+            else
+                st_hint(reinterpret_cast<float4*>(p.ws_o + ws_slot(p, row, part) * D + 4 * c4), v, l2_evict_last());
+        }
+        if (!final_out && qd == 0) {
+#pragma unroll
+            for (int hr = 0; hr < NHT; ++hr)
+                if (r + 8 * hr < GC)
+                    st_hint(reinterpret_cast<float2*>(
+                                p.ws_ml + ws_slot(p, ragged_row(it, p.G, p.H_q, g, 16 * hg + r + 8 * hr), part) * 2),
+                            make_float2(m_run[hr], l_run[hr]), l2_evict_last());
+        }
+        return;
+    }
     const size_t row0 = (size_t)b * p.H_q + hbase;
     float* dst = final_out ? p.out : p.ws_o;
     for (int i = lane; i < GC * (D / 4); i += 32) {
@@ -655,12 +718,12 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
     }
 }
 
-template <int DT, int D>
+template <int DT, int D, bool RAG>
 int launch_q(const DecodeParams& p, int nht, dim3 grid, cudaStream_t s, const CUtensorMap* tmk, const CUtensorMap* tmv)
 {
     const int smem = QCfg<DT, D>::BODY + 1024 + (p.part_tokens / kBlock) * (int)(sizeof(float2) + sizeof(int));
-    auto k1 = decode_mmaq_kernel<DT, D, 1>;
-    auto k2 = decode_mmaq_kernel<DT, D, 2>;
+    auto k1 = decode_mmaq_kernel<DT, D, 1, RAG>;
+    auto k2 = decode_mmaq_kernel<DT, D, 2, RAG>;
     auto kern = nht == 1 ? k1 : k2;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return PKV_ERR_CUDA;
@@ -668,20 +731,33 @@ int launch_q(const DecodeParams& p, int nht, dim3 grid, cudaStream_t s, const CU
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
+template <bool RAG>
+int launch_q_any(const DecodeParams& p, int kv_dtype, int d, int nht, dim3 grid, cudaStream_t s,
+                 const CUtensorMap* tmk, const CUtensorMap* tmv)
+{
+    switch (kv_dtype * 1000 + d) {
+    case PKV_INT8 * 1000 + 128: return launch_q<PKV_INT8, 128, RAG>(p, nht, grid, s, tmk, tmv);
+    case PKV_INT8 * 1000 + 64: return launch_q<PKV_INT8, 64, RAG>(p, nht, grid, s, tmk, tmv);
+    case PKV_FP8E4M3 * 1000 + 128: return launch_q<PKV_FP8E4M3, 128, RAG>(p, nht, grid, s, tmk, tmv);
+    case PKV_FP8E4M3 * 1000 + 64: return launch_q<PKV_FP8E4M3, 64, RAG>(p, nht, grid, s, tmk, tmv);
+    case PKV_INT4 * 1000 + 128: return launch_q<PKV_INT4, 128, RAG>(p, nht, grid, s, tmk, tmv);
+    case PKV_INT4 * 1000 + 64: return launch_q<PKV_INT4, 64, RAG>(p, nht, grid, s, tmk, tmv);
+    default: return PKV_ERR_UNSUPPORTED;
+    }
+}
+
 }  // namespace
 
 int launch_decode_quant(const DecodeParams& p, int kv_dtype, int d, int nht, dim3 grid, cudaStream_t s,
                         const CUtensorMap* tmk, const CUtensorMap* tmv)
 {
-    switch (kv_dtype * 1000 + d) {
-    case PKV_INT8 * 1000 + 128: return launch_q<PKV_INT8, 128>(p, nht, grid, s, tmk, tmv);
-    case PKV_INT8 * 1000 + 64: return launch_q<PKV_INT8, 64>(p, nht, grid, s, tmk, tmv);
-    case PKV_FP8E4M3 * 1000 + 128: return launch_q<PKV_FP8E4M3, 128>(p, nht, grid, s, tmk, tmv);
-    case PKV_FP8E4M3 * 1000 + 64: return launch_q<PKV_FP8E4M3, 64>(p, nht, grid, s, tmk, tmv);
-    case PKV_INT4 * 1000 + 128: return launch_q<PKV_INT4, 128>(p, nht, grid, s, tmk, tmv);
-    case PKV_INT4 * 1000 + 64: return launch_q<PKV_INT4, 64>(p, nht, grid, s, tmk, tmv);
-    default: return PKV_ERR_UNSUPPORTED;
-    }
+    return launch_q_any<false>(p, kv_dtype, d, nht, grid, s, tmk, tmv);
+}
+
+int launch_decode_quant_ragged(const DecodeParams& p, int kv_dtype, int d, int nht, dim3 grid, cudaStream_t s,
+                               const CUtensorMap* tmk, const CUtensorMap* tmv)
+{
+    return launch_q_any<true>(p, kv_dtype, d, nht, grid, s, tmk, tmv);
 }
 
 }  // namespace pkv

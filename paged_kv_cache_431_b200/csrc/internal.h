@@ -126,6 +126,38 @@ int launch_prefill(const PrefillArgs& a, const CUtensorMap* tmk, const CUtensorM
 // follow their own rule.
 int decode_keys_tc_available(int d, int G, int kv_dtype);
 
+// One launch of the ragged form (decode_common.cuh, RaggedMode): items that are runs of query
+// rows sharing their keys.
+struct RaggedArgs {
+    int mode;
+    const void* q;
+    int q_dtype;
+    const int32_t* tables;
+    int W;
+    const int32_t* ctx_lens;
+    const int32_t* row_starts;
+    const int32_t* prefix_lens;
+    int items;              // grid items: sequences, or groups
+    int starts;             // row_starts has starts + 1 entries
+    int total_rows, max_rows;
+    int H_q, H_kv, G, N, d, kv_dtype;
+    int part_tokens, max_parts;
+    int part_base, slots;   // first workspace slot of this launch, slots per row
+    int max_prefix, pre_part;
+    float scale;
+    const float* k_scale;
+    const float* v_scale;
+    void* out;
+    float* ws_o;            // [total_rows][H_q][slots][d]
+    float* ws_ml;           // [total_rows][H_q][slots][2]
+    int32_t* status;
+};
+
+// Few query rows per item: warp-level MMAs, bound by the K/V bytes (decode.cu, decode_quant.cu).
+int launch_ragged_short(const RaggedArgs& a, const CUtensorMap* tmk, const CUtensorMap* tmv, cudaStream_t s);
+// Merge of the partials of a kCross launch, or of a kPrefix and a kSuffix launch (args of the latter).
+int launch_ragged_merge(const RaggedArgs& a, cudaStream_t s);
+
 using PFN_encode = PFN_cuTensorMapEncodeTiled_v12000;
 PFN_encode tensor_map_encoder();   // null when no driver is present
 

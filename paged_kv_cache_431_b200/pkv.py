@@ -87,6 +87,14 @@ def lib() -> ctypes.CDLL:
     L.kv_append_rope_workspace_bytes.argtypes = [P, i32]
     L.kv_append_rope.restype = i32
     L.kv_append_rope.argtypes = [P, i32, P, i64, P, i64, P, i64, i32, P, P, P, i32, i32, P, i64, P, sz, P]
+    L.paged_cross_workspace_bytes.restype = sz
+    L.paged_cross_workspace_bytes.argtypes = [P, i32, i32, i32, i32, i32]
+    L.paged_cross_attn.restype = i32
+    L.paged_cross_attn.argtypes = [P, i32, P, i32, P, i32, i32, P, i32, P, i32, i32, i32, f32, P, P, sz, P]
+    L.paged_decode_groups_workspace_bytes.restype = sz
+    L.paged_decode_groups_workspace_bytes.argtypes = [P, i32, i32, i32, i32, i32, i32]
+    L.paged_decode_attn_groups.restype = i32
+    L.paged_decode_attn_groups.argtypes = [P, i32, P, i32, P, i32, P, i32, i32, P, P, i32, i32, i32, i32, f32, P, P, sz, P]
     L.paged_decode_workspace_bytes.restype = sz
     L.paged_decode_workspace_bytes.argtypes = [P, i32, i32, i32, P]
     L.paged_decode_attn.restype = i32
@@ -430,6 +438,93 @@ def paged_decode_attn_cascade(pool: KVPool, layer: int, q: torch.Tensor, block_t
               _ptr(context_lens), B, H_q, max_context_len, shared_prefix_len, float(scale), _ptr(out),
               _ptr(workspace), ws_bytes, _opts(engine, partition_tokens, sliding_window), _stream(stream)),
            "paged_decode_attn_cascade")
+    return out
+
+
+def _ragged_out(on, q, out):
+    if not q.is_contiguous() or q.dim() != 3:
+        raise ValueError("q: expected a contiguous [rows, H_q, head_dim] tensor")
+    if out is None:
+        out = torch.empty_like(q)
+        on.keep(out)
+    if out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor of q's shape and dtype")
+    return out
+
+
+def _tables(t: torch.Tensor, n: int):
+    if t.dim() != 2 or t.shape[0] != n:
+        raise ValueError(f"block_tables: expected [{n}, width]")
+    return _int32(t, None, "block_tables")
+
+
+def _check_head_dim(pool: KVPool, q: torch.Tensor):
+    if q.shape[2] != pool.head_dim:
+        raise ValueError(f"q has head dim {q.shape[2]}, the pool {pool.head_dim}")
+
+
+def _ws(on, workspace, need: int):
+    if need and workspace is None:
+        workspace = on.empty(need)
+    return _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0
+
+
+def paged_cross_workspace_bytes(pool: KVPool, total_rows: int, num_q_heads: int, num_seqs: int, max_rows: int,
+                                max_context_len: int) -> int:
+    return int(lib().paged_cross_workspace_bytes(pool.handle, total_rows, num_q_heads, num_seqs, max_rows,
+                                                 max_context_len))
+
+
+def paged_cross_attn(pool: KVPool, layer: int, q: torch.Tensor, row_starts: torch.Tensor, block_tables: torch.Tensor,
+                     context_lens: torch.Tensor, scale: float, max_rows: int, max_context_len: int,
+                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """Attention of a ragged batch of rows q [rows, H_q, head_dim] to all cached tokens of their
+    sequences: rows row_starts[b] .. row_starts[b+1]-1 belong to sequence b (int32 [B + 1]).
+    Returns out in q's dtype; rows of no sequence are left as they are."""
+    dev = _pool_device(pool)
+    with _OnDevice(dev, stream, q, row_starts, block_tables, context_lens, out, workspace) as on:
+        out = _ragged_out(on, q, out)
+        _check_head_dim(pool, q)
+        rows, H_q, _ = q.shape
+        B = context_lens.shape[0]
+        wp, wb = _ws(on, workspace, paged_cross_workspace_bytes(pool, rows, H_q, B, max_rows, max_context_len))
+        _check(lib().paged_cross_attn(pool.handle, layer, _ptr(q), _dtype_code(q),
+                                      _int32(row_starts, B + 1, "row_starts"), rows, H_q, _tables(block_tables, B),
+                                      block_tables.shape[1], _int32(context_lens, B, "context_lens"), B, max_rows,
+                                      max_context_len, float(scale), _ptr(out), wp, wb, on.stream()),
+               "paged_cross_attn")
+    return out
+
+
+def paged_decode_groups_workspace_bytes(pool: KVPool, num_seqs: int, num_q_heads: int, num_groups: int,
+                                        max_group_size: int, max_prefix_len: int, max_suffix_len: int) -> int:
+    return int(lib().paged_decode_groups_workspace_bytes(pool.handle, num_seqs, num_q_heads, num_groups,
+                                                         max_group_size, max_prefix_len, max_suffix_len))
+
+
+def paged_decode_attn_groups(pool: KVPool, layer: int, q: torch.Tensor, block_tables: torch.Tensor,
+                             context_lens: torch.Tensor, group_starts: torch.Tensor, prefix_lens: torch.Tensor,
+                             scale: float, max_group_size: int, max_prefix_len: int, max_suffix_len: int,
+                             out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                             stream=None) -> torch.Tensor:
+    """Decode attention for a batch in groups: sequences group_starts[g] .. group_starts[g+1]-1
+    (int32 [groups + 1]) share their first prefix_lens[g] tokens, a multiple of 16.  Returns out
+    [B, H_q, head_dim] in q's dtype; rows of sequences in no group are left as they are."""
+    dev = _pool_device(pool)
+    with _OnDevice(dev, stream, q, block_tables, context_lens, group_starts, prefix_lens, out, workspace) as on:
+        out = _ragged_out(on, q, out)
+        _check_head_dim(pool, q)
+        B, H_q, _ = q.shape
+        n = prefix_lens.shape[0]
+        wp, wb = _ws(on, workspace, paged_decode_groups_workspace_bytes(pool, B, H_q, n, max_group_size,
+                                                                        max_prefix_len, max_suffix_len))
+        _check(lib().paged_decode_attn_groups(pool.handle, layer, _ptr(q), _dtype_code(q), _tables(block_tables, B),
+                                              block_tables.shape[1], _int32(context_lens, B, "context_lens"), B, H_q,
+                                              _int32(group_starts, n + 1, "group_starts"),
+                                              _int32(prefix_lens, n, "prefix_lens"), n, max_group_size,
+                                              max_prefix_len, max_suffix_len, float(scale), _ptr(out), wp, wb,
+                                              on.stream()), "paged_decode_attn_groups")
     return out
 
 
