@@ -628,18 +628,46 @@ int paged_decode_attn_cascade(pkv_pool_t pool, int layer, const void* q, int q_d
 
 // ---- ragged batches: cross attention, decode over groups with prefixes ----------------
 
-// How a ragged launch splits the keys: tokens per partition and the partitions of the longest item.
+// How a ragged launch runs: the kernel, tokens per partition, and the partitions of the longest item.
 struct RaggedSplit {
+    bool tc, pair;
     int part, parts;
 };
+
+// Items of up to this many query rows per KV head run on the warp-level kernels, above on tcgen05.
+constexpr int kShortRows16 = 64;       // 16-bit pools: one K/V ring serves 64 rows
+constexpr int kShortRowsQuant = 16;    // quantized: each 16 rows read and convert the codes again
 
 static RaggedSplit ragged_split(pkv_pool_t pool, int items, int max_rows, int G, int max_tokens)
 {
     RaggedSplit r;
-    const int ctas = pool->d.num_kv_heads * ((max_rows * G + 15) / 16);
-    r.part = choose_partition(items, ctas, max_tokens, pool->row_bytes, is_quantized(pool->d.kv_dtype), nullptr);
-    r.parts = max_tokens > 0 ? (max_tokens + r.part - 1) / r.part : 1;
+    const bool quant = is_quantized(pool->d.kv_dtype);
+    const long long R = (long long)max_rows * G;
+    const int H_kv = pool->d.num_kv_heads;
+    r.tc = R > (quant ? kShortRowsQuant : kShortRows16);
+    r.pair = r.tc && R <= 128;
+    if (!r.tc) {
+        r.part = choose_partition(items, H_kv * (int)((R + 15) / 16), max_tokens, pool->row_bytes, quant, nullptr);
+    } else {
+        // one CTA per SM: split the keys until two waves are full, in whole 128-key tiles, at
+        // least two of them per partition
+        const long long ctas = (long long)items * H_kv * ((R + (r.pair ? 127 : 255)) / (r.pair ? 128 : 256));
+        long long parts = 2LL * num_sms() / (ctas > 0 ? ctas : 1);
+        parts = (parts < 1 ? 1 : parts) * (r.pair ? 2 : 1);
+        const long long most = (max_tokens + 255) / 256;
+        parts = parts > most ? (most < 1 ? 1 : most) : parts;
+        r.part = (int)((((long long)max_tokens + parts - 1) / parts + 127) / 128 * 128);
+        if (r.part < 128) r.part = 128;
+    }
+    r.parts = max_tokens > 0 ? (int)(((long long)max_tokens + r.part - 1) / r.part) : 1;
     return r;
+}
+
+static int launch_ragged(const RaggedArgs& a, const RaggedSplit& sp, const CUtensorMap* tmk, const CUtensorMap* tmv,
+                         cudaStream_t s)
+{
+    if (!sp.tc) return launch_ragged_short(a, tmk, tmv, s);
+    return launch_ragged_tc(a, sp.pair, tmk, tmv, s);
 }
 
 static size_t ragged_ws_bytes(pkv_pool_t pool, int rows, int num_q_heads, int slots)
@@ -736,7 +764,7 @@ int paged_cross_attn(pkv_pool_t pool, int layer, const void* q, int q_dtype, con
     a.ws_o = need ? static_cast<float*>(workspace) : nullptr;
     a.ws_ml = need ? a.ws_o + (size_t)total_rows * num_q_heads * sp.parts * a.d : nullptr;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    rc = launch_ragged_short(a, tmk, tmv, s);
+    rc = launch_ragged(a, sp, tmk, tmv, s);
     if (rc != PKV_OK || sp.parts <= 1) return rc;
     return launch_ragged_merge(a, s);
 }
@@ -771,7 +799,7 @@ int paged_decode_attn_groups(pkv_pool_t pool, int layer, const void* q, int q_dt
     RaggedArgs a = ragged_args(pool, layer, q, q_dtype, num_q_heads, scale, num_seqs, block_tables, block_table_width,
                                context_lens, group_starts, out);
     const RaggedSplit pre = max_prefix_len > 0 ? ragged_split(pool, num_groups, max_group_size, a.G, max_prefix_len)
-                                               : RaggedSplit{PKV_BLOCK_SIZE, 0};
+                                               : RaggedSplit{false, false, PKV_BLOCK_SIZE, 0};
     const RaggedSplit own = ragged_split(pool, num_seqs, 1, a.G, max_suffix_len);
     const int slots = pre.parts + own.parts;
     const size_t need = slots > 1 ? ragged_ws_bytes(pool, num_seqs, num_q_heads, slots) : 0;
@@ -794,7 +822,7 @@ int paged_decode_attn_groups(pkv_pool_t pool, int layer, const void* q, int q_dt
         a.max_rows = max_group_size;
         a.part_tokens = pre.part;
         a.max_parts = pre.parts;
-        rc = launch_ragged_short(a, tmk, tmv, s);
+        rc = launch_ragged(a, pre, tmk, tmv, s);
         if (rc != PKV_OK) return rc;
     }
     // 2. every sequence's own tokens, 3. the merge of both
@@ -805,7 +833,7 @@ int paged_decode_attn_groups(pkv_pool_t pool, int layer, const void* q, int q_dt
     a.max_parts = own.parts;
     a.part_base = pre.parts;
     a.pre_part = pre.part;
-    rc = launch_ragged_short(a, tmk, tmv, s);
+    rc = launch_ragged(a, own, tmk, tmv, s);
     if (rc != PKV_OK || slots <= 1) return rc;
     return launch_ragged_merge(a, s);
 }

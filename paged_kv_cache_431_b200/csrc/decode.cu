@@ -810,6 +810,18 @@ int launch_ragged_short(const RaggedArgs& a, const CUtensorMap* tmk, const CUten
               : launch_mma16<64, false, true>(p, nht, grid, s, tmk, tmv);
 }
 
+int launch_ragged_tc(const RaggedArgs& a, bool pair, const CUtensorMap* tmk, const CUtensorMap* tmv, cudaStream_t s)
+{
+    const DecodeParams p = ragged_params(a);
+    switch (a.kv_dtype) {
+    case PKV_BF16: return launch_ragged_tc_bf16(p, a.d, pair, a.items, a.max_rows, tmk, tmv, s);
+    case PKV_F16: return launch_ragged_tc_f16(p, a.d, pair, a.items, a.max_rows, tmk, tmv, s);
+    case PKV_INT8: return launch_ragged_tc_int8(p, a.d, pair, a.items, a.max_rows, tmk, tmv, s);
+    case PKV_INT4: return launch_ragged_tc_int4(p, a.d, pair, a.items, a.max_rows, tmk, tmv, s);
+    default: return launch_ragged_tc_fp8(p, a.d, pair, a.items, a.max_rows, tmk, tmv, s);
+    }
+}
+
 int launch_ragged_merge(const RaggedArgs& a, cudaStream_t s)
 {
     const DecodeParams p = ragged_params(a);

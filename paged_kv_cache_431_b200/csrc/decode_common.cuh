@@ -221,6 +221,18 @@ int launch_decode_tc_fp8(const DecodeParams& p, const CUtensorMap* tmk, const CU
 // Launch the quantized-pool decode kernel (decode_quant.cu).
 int launch_decode_quant(const DecodeParams& p, int kv_dtype, int d, int nht, dim3 grid, cudaStream_t s,
                         const CUtensorMap* tmk, const CUtensorMap* tmv);
+// tcgen05 kernel of the ragged form, one file per pool dtype (ragged_tc.cuh).
+int launch_ragged_tc_bf16(const DecodeParams& p, int d, bool pair, int items, int max_rows, const CUtensorMap* tmk,
+                          const CUtensorMap* tmv, cudaStream_t s);
+int launch_ragged_tc_f16(const DecodeParams& p, int d, bool pair, int items, int max_rows, const CUtensorMap* tmk,
+                         const CUtensorMap* tmv, cudaStream_t s);
+int launch_ragged_tc_int8(const DecodeParams& p, int d, bool pair, int items, int max_rows, const CUtensorMap* tmk,
+                          const CUtensorMap* tmv, cudaStream_t s);
+int launch_ragged_tc_int4(const DecodeParams& p, int d, bool pair, int items, int max_rows, const CUtensorMap* tmk,
+                          const CUtensorMap* tmv, cudaStream_t s);
+int launch_ragged_tc_fp8(const DecodeParams& p, int d, bool pair, int items, int max_rows, const CUtensorMap* tmk,
+                         const CUtensorMap* tmv, cudaStream_t s);
+
 // The same kernels over ragged items (decode.cu, decode_quant.cu).
 int launch_decode_quant_ragged(const DecodeParams& p, int kv_dtype, int d, int nht, dim3 grid, cudaStream_t s,
                                const CUtensorMap* tmk, const CUtensorMap* tmv);

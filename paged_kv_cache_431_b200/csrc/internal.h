@@ -155,6 +155,9 @@ struct RaggedArgs {
 
 // Few query rows per item: warp-level MMAs, bound by the K/V bytes (decode.cu, decode_quant.cu).
 int launch_ragged_short(const RaggedArgs& a, const CUtensorMap* tmk, const CUtensorMap* tmv, cudaStream_t s);
+// Many query rows per item: tcgen05 (ragged_tc.cuh).  pair: at most 128 query rows per KV head,
+// two partitions per CTA.  part_tokens a multiple of 128.
+int launch_ragged_tc(const RaggedArgs& a, bool pair, const CUtensorMap* tmk, const CUtensorMap* tmv, cudaStream_t s);
 // Merge of the partials of a kCross launch, or of a kPrefix and a kSuffix launch (args of the latter).
 int launch_ragged_merge(const RaggedArgs& a, cudaStream_t s);
 

@@ -1,0 +1,704 @@
+// ragged_tc.cuh -- the ragged operators (paged_cross_attn, paged_decode_attn_groups) on the 5th-generation tensor cores (tcgen05 + TMEM).
+//
+// Rows of one item (a sequence's query rows, or a group's sequences) all see the same keys, so
+// with R = rows x G query rows per KV head this is a dense [R x keys] contraction:
+//   S = Q.K^T,  P = 2^(scale S - m),  O += P.V,  out = O / sum P
+// One CTA (one per SM) holds two query tiles A and B of 128 rows in flight, so that the tensor
+// cores work on one while the softmax warps work on the other:
+//   !PAIR  A and B are 256 consecutive rows that share every K/V tile (bound by the tensor cores
+//          and by the exponentials: 2 x 128 x 128 of them per key tile on 16 lanes a cycle are as
+//          many cycles as the four MMAs);
+//   PAIR   (at most 128 rows per item and KV head: bound by the K/V bytes) A and B are the SAME
+//          rows against two key partitions, each with its own K/V tiles; both write partials.
+// Warps: 0 fetches (TMA, one box per paged block and 64 dims), 1 issues every MMA, 2..5 and 6..9
+// are the softmax of A and B (one thread per query row = TMEM lane); for quantized pools 10..13
+// turn fetched code tiles into fp16 tiles (the codes are exact in fp16; the K scale of a (block,
+// head) multiplies its 16 scores, its V scale multiplies P, so a tile is converted once for all
+// rows).  Per key tile and query tile: S (128 columns of TMEM) -> P back over the same columns as
+// 16-bit pairs, the A operand of P.V, in two halves of 64 keys so that P.V starts while the other
+// half is exponentiated.  The running max is lazy: O is rescaled only when a new max exceeds the
+// old by 2^8.
+//
+// Roundings: Q, K, V enter as they are (16-bit; codes in fp16; a quantized pool's q in fp16
+// after a power of two per row that brings its largest element to [1, 2), exact for bf16 down to
+// 2^-17 of that).  S, m, sum P and O are fp32.  P enters P.V rounded to nearest in ONE 16-bit part:
+// the output is rounded to 16 bits anyway, and P's half step (2^-9 for bf16, 2^-12 for fp16),
+// spread over the keys, is of that size (measured against 64 bits: 1.4 times the error of an
+// output that is only rounded).  The fp32-output kernels keep two parts.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "decode_common.cuh"
+#include "tcgen05.cuh"
+
+namespace pkv {
+
+namespace ragged {
+
+constexpr int kBM = 128;                         // query rows per tile
+constexpr int kBN = 128;                         // keys per tile
+constexpr int kBlocks = kBN / kBlock;            // paged blocks per key tile
+constexpr float kSlack = 8.f;                    // log2 units the running max may lag
+constexpr uint32_t kTmemCols = 512;              // tile x: S and P at 256x, O at 256x + 128
+constexpr int kScaleSlots = 4;                   // key tiles whose scales are kept
+
+template <int D, int DT, bool PAIR>
+struct Cfg {
+    static constexpr bool QUANT = DT == PKV_INT8 || DT == PKV_INT4 || DT == PKV_FP8E4M3;
+    static constexpr bool BF16 = DT == PKV_BF16;                  // MMA operand type (else fp16)
+    static constexpr int HALVES = D / 64;                         // 64-dim column groups
+    static constexpr int TILE = kBN * D * 2;                      // one 16-bit Q, K or V tile
+    static constexpr int QT = PAIR ? 1 : 2;                       // Q tiles
+    static constexpr int ROW = DT == PKV_INT4 ? D / 2 : D;        // code bytes per row
+    static constexpr int CTILE = QUANT ? kBN * ROW : 0;           // one code tile
+    // ring depths: what 227 KB hold; 16-bit pools fetch into the K/V rings themselves
+    static constexpr int NS = QUANT ? 2 : (D == 64 ? 4 : PAIR ? 3 : 2);
+    static constexpr int NC = QUANT ? (PAIR || D == 64 ? 2 : DT == PKV_INT4 ? 2 : 1) : 1;
+    static constexpr int SMEM = QT * TILE + NS * 2 * TILE + NC * 2 * CTILE + 1024;
+    static constexpr int THREADS = QUANT ? 448 : 320;
+    static constexpr int SWZ = ROW >= 128 ? 7 : ROW == 64 ? 3 : 1;   // TMA swizzle of a code tile
+    static_assert(SMEM <= 225 * 1024, "dynamic shared memory, with 2 KB left for the static part");
+};
+
+struct Bars {
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];    // 16-bit tiles, ready for the MMAs
+    uint64_t ck_full[2], ck_empty[2], cv_full[2], cv_empty[2];   // code tiles
+    uint64_t sc_full[kScaleSlots];
+    uint64_t s_full[2];        // S(x, t) is in TMEM, and every earlier MMA of the CTA is done
+    uint64_t p_full[2][2];     // a half of P(x, t) is stored
+    uint64_t o_done[2];
+    uint64_t mma_drain;
+};
+
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b)
+{
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2bits(a)), "l"(f2bits(b)));
+    return bitsf2(d);
+}
+
+__device__ __forceinline__ float exp2_int(int e) { return __int_as_float((127 + e) << 23); }   // e in [-126, 127]
+
+// Exponent shift that brings x > 0 to [1, 2), kept in [-100, 100]; 0 for x = 0.
+__device__ __forceinline__ int unit_shift(float x)
+{
+    if (!(x > 0.f)) return 0;
+    const int e = (int)((__float_as_uint(x) >> 23) & 0xffu) - 127;
+    return max(-100, min(100, -e));
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ uint32_t hsub2_const(uint32_t a, float c)
+{
+    __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), __float2half2_rn(c));
+    return *reinterpret_cast<uint32_t*>(&r);
+}
+
+// Four 8-bit codes -> two fp16 pairs, exact.  int8: code + 128 moved into the significand of
+// 1024, then 1152 subtracted.
+template <int DT>
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t& a, uint32_t& b)
+{
+    if constexpr (DT == PKV_INT8) {
+        const uint32_t x = w ^ 0x80808080u;
+        a = hsub2_const(__byte_perm(x, 0x64646464u, 0x4140), 1152.f);
+        b = hsub2_const(__byte_perm(x, 0x64646464u, 0x4342), 1152.f);
+    } else {
+        const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+        const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+        a = (uint32_t)lo.x | ((uint32_t)lo.y << 16);
+        b = (uint32_t)hi.x | ((uint32_t)hi.y << 16);
+    }
+}
+
+// Eight 4-bit codes -> four fp16 pairs in order, exact.  Nibbles 2i and 2i + 1 are brought to
+// bits 0..3 of two halves, code + 8 moved into the significand of 1024, then 1032 subtracted.
+__device__ __forceinline__ void codes8_int4(uint32_t w, uint32_t (&h)[4])
+{
+    const uint32_t x = w ^ 0x88888888u;
+    const uint32_t even = x & 0x0f0f0f0fu, odd = (x >> 4) & 0x0f0f0f0fu;   // byte i: elements 2i, 2i + 1
+    const uint32_t p01 = __byte_perm(even, odd, 0x5140), p23 = __byte_perm(even, odd, 0x7362);
+    h[0] = hsub2_const(__byte_perm(p01, 0x64646464u, 0x4140), 1032.f);
+    h[1] = hsub2_const(__byte_perm(p01, 0x64646464u, 0x4342), 1032.f);
+    h[2] = hsub2_const(__byte_perm(p23, 0x64646464u, 0x4140), 1032.f);
+    h[3] = hsub2_const(__byte_perm(p23, 0x64646464u, 0x4342), 1032.f);
+}
+
+template <int D, int DT, bool PAIR>
+__global__ void __launch_bounds__((Cfg<D, DT, PAIR>::THREADS), 1)
+ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV)
+{
+    using C = Cfg<D, DT, PAIR>;
+    constexpr int NS = C::NS, NC = C::NC, TILE = C::TILE;
+    extern __shared__ uint8_t smem_dyn[];
+    __shared__ Bars bars;
+    __shared__ uint32_t s_tmem_base;
+    __shared__ volatile int s_abort;
+    __shared__ float s_rowscale[C::QUANT ? C::QT * kBM : 1];              // per query row: 2^-e of its fp16 q
+    __shared__ __align__(8) float2 s_scale[C::QUANT ? kScaleSlots * kBlocks : 1];   // (K, V) scales of a key tile's blocks
+    __shared__ int s_vmax;
+
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = blockIdx.y;
+    const int zparts = PAIR ? (p.max_parts + 1) / 2 : p.max_parts;
+    const int b = blockIdx.z / zparts, z = blockIdx.z % zparts;
+    const RaggedItem it = ragged_item(p.rg, p.ctx_lens, p.W, p.max_parts * p.part_tokens, b, p.status,
+                                      threadIdx.x == 0 && blockIdx.x == 0 && z == 0 && g == 0);
+    const int R = it.rows * p.G;                                  // query rows of this KV head
+    const int r0 = blockIdx.x * (C::QT * kBM);
+    if (r0 >= R) return;
+    const int nparts = (it.end - it.base + p.part_tokens - 1) / p.part_tokens;
+    const int part0 = PAIR ? 2 * z : z;                           // partition of tile A
+    if (part0 >= nparts) {
+        if (z == 0 && it.whole) {                                 // no keys at all: zero rows
+            const int n = min(C::QT * kBM, R - r0) * (D / 8);
+            for (int i = threadIdx.x; i < n; i += C::THREADS)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.rg.out16) +
+                                          ragged_row(it, p.G, p.H_q, g, r0 + i / (D / 8)) * D + 8 * (i % (D / 8))) =
+                    make_uint4(0u, 0u, 0u, 0u);
+        }
+        return;
+    }
+    // Tile x: key range [key_lo(x), key_hi(x)) in ntiles(x) key tiles.  `shared`: both query tiles
+    // use every K/V tile; else K/V tiles come in the order (A,0) (B,0) (A,1) (B,1) ...
+    const bool shared = !PAIR && r0 + kBM < R;
+    auto key_lo = [&](int x) { return it.base + (PAIR ? part0 + x : part0) * p.part_tokens; };
+    auto key_hi = [&](int x) { return min(it.end, key_lo(x) + p.part_tokens); };
+    auto ntiles = [&](int x) {
+        if (!PAIR && x == 1 && !shared) return 0;
+        return max(0, (key_hi(x) - key_lo(x) + kBN - 1) / kBN);
+    };
+    const int nA = ntiles(0), nB = ntiles(1);
+    const int nseq = shared ? nA : nA + nB;                       // K/V tiles of this CTA
+    auto seq = [&](int x, int t) { return shared ? t : x == 0 ? t + min(t, nB) : t + min(t + 1, nA); };
+
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+    const uint32_t sQ = smem_u32(smem);
+    const uint32_t sK = sQ + C::QT * TILE;
+    const uint32_t sV = sK + NS * TILE;
+    const uint32_t sCK = sV + NS * TILE;
+    const uint32_t sCV = sCK + NC * C::CTILE;
+
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        s_vmax = 0;
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(smem_u32(&bars.k_full[s]), C::QUANT ? 4 : 1);
+            mbar_init(smem_u32(&bars.k_empty[s]), 1);
+            mbar_init(smem_u32(&bars.v_full[s]), C::QUANT ? 4 : 1);
+            mbar_init(smem_u32(&bars.v_empty[s]), 1);
+        }
+        if constexpr (C::QUANT) {
+            for (int s = 0; s < NC; ++s) {
+                mbar_init(smem_u32(&bars.ck_full[s]), 1);
+                mbar_init(smem_u32(&bars.ck_empty[s]), 4);
+                mbar_init(smem_u32(&bars.cv_full[s]), 1);
+                mbar_init(smem_u32(&bars.cv_empty[s]), 4);
+            }
+            for (int s = 0; s < kScaleSlots; ++s) mbar_init(smem_u32(&bars.sc_full[s]), 4);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(smem_u32(&bars.s_full[x]), 1);
+            mbar_init(smem_u32(&bars.p_full[x][0]), 4);
+            mbar_init(smem_u32(&bars.p_full[x][1]), 4);
+            mbar_init(smem_u32(&bars.o_done[x]), 1);
+        }
+        mbar_init(smem_u32(&bars.mma_drain), 1);
+        mbar_fence_init();
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem_base)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    const int32_t* trow = p.tables + (size_t)it.table * p.W;
+    auto block_id = [&](int lb) -> int {       // physical block of logical block lb (in bounds)
+        int blk = trow[lb];
+        if ((unsigned)blk >= (unsigned)p.N) {
+            flag_status(p.status, PKV_DEV_BAD_BLOCK);
+            blk = 0;
+        }
+        return blk;
+    };
+    __syncthreads();                            // s_vmax and the barriers are initialised
+
+    // ---- Q into shared memory, K-major with the 128-byte swizzle, by plain loads: rows are
+    // gathered (row of the item, head), so any group size packs 128 rows into a tile.  A negative
+    // scale is moved into q, so that the softmax may take maxima before it scales.
+    {
+        constexpr int CH = D / 8;               // 16-byte chunks per row
+        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+        const uint16_t* qh = static_cast<const uint16_t*>(p.q);
+        for (int i = threadIdx.x; i < ((C::QT * kBM * CH + C::THREADS - 1) / C::THREADS) * C::THREADS; i += C::THREADS) {
+            const int row = i / CH, c = i % CH;
+            const bool in = row < C::QT * kBM && r0 + row < R;
+            uint4 u = make_uint4(0u, 0u, 0u, 0u);
+            if (in) u = __ldg(reinterpret_cast<const uint4*>(qh + ragged_row(it, p.G, p.H_q, g, r0 + row) * D + 8 * c));
+            uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+            if constexpr (C::QUANT) {           // fp16, times a power of two per row (its CH lanes agree on it)
+                float f[8], top = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 v = p.q_bf16 ? unpack2<true>(w[e]) : unpack2<false>(w[e]);
+                    f[2 * e] = v.x;
+                    f[2 * e + 1] = v.y;
+                    top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+                }
+#pragma unroll
+                for (int o = CH / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const int e = unit_shift(top);
+                const float m = exp2_int(e);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = pack2<false>(f[2 * k] * m, f[2 * k + 1] * m);
+                if (row < C::QT * kBM && c == 0) s_rowscale[row] = exp2_int(-e);
+            }
+            if (row < C::QT * kBM) {
+                const int tile = row / kBM, rr = row % kBM;
+                sts128(sQ + tile * TILE + (c >> 3) * (kBM * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), w[0] ^ flip,
+                       w[1] ^ flip, w[2] ^ flip, w[3] ^ flip);
+            }
+        }
+        fence_proxy_async_smem();
+    }
+    // ---- the largest V scale of the CTA's keys: P enters P.V times (V scale / its power of two)
+    if constexpr (C::QUANT) {
+        const int lb0 = key_lo(0) / kBlock, lb1 = (max(key_hi(0), nB > 0 ? key_hi(1) : 0) + kBlock - 1) / kBlock;
+        float m = 0.f;
+        for (int lb = lb0 + threadIdx.x; lb < lb1; lb += C::THREADS)
+            m = fmaxf(m, p.v_scale[(size_t)block_id(lb) * p.H_kv + g]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane == 0) atomicMax(&s_vmax, __float_as_int(m));     // non-negative: ordered as integers
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem_base;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        // The lanes hold the block ids of the next 4 key tiles of A and of B (one load per 4 tiles,
+        // a chunk ahead); lane 0 issues the copies.  Keys past the range fetch block 0: in bounds,
+        // masked, and their V rows zeroed.
+        int cur[2], nxt[2];
+        auto entry = [&](int x, int i) -> int {
+            const int lb = key_lo(x) / kBlock + i;
+            return lb * kBlock < key_hi(x) ? block_id(lb) : 0;
+        };
+        for (int x = 0; x < 2; ++x) {
+            cur[x] = (x == 0 || nB > 0) ? entry(x, lane) : 0;
+            nxt[x] = (x == 0 || nB > 0) ? entry(x, 32 + lane) : 0;
+        }
+        constexpr int ND = C::QUANT ? NC : NS;                    // depth of the rings the copies go to
+        uint64_t* kf = C::QUANT ? bars.ck_full : bars.k_full;
+        uint64_t* ke = C::QUANT ? bars.ck_empty : bars.k_empty;
+        uint64_t* vf = C::QUANT ? bars.cv_full : bars.v_full;
+        uint64_t* ve = C::QUANT ? bars.cv_empty : bars.v_empty;
+        constexpr uint32_t BYTES = C::QUANT ? C::CTILE : TILE;
+        const uint32_t kdst = C::QUANT ? sCK : sK, vdst = C::QUANT ? sCV : sV;
+        int issued_k = 0, issued_v = 0;
+        bool go = true;
+        const uint64_t pol = l2_evict_first();
+        auto fetch = [&](const CUtensorMap* tm, uint32_t dst, const int (&rows)[kBlocks], uint32_t bar) {
+            mbar_arrive_expect_tx(bar, BYTES);
+#pragma unroll
+            for (int kb = 0; kb < kBlocks; ++kb) {
+                if constexpr (C::QUANT) {
+                    if constexpr (PAIR) tma_load_2d_hint(dst + kb * kBlock * C::ROW, tm, 0, rows[kb], bar, pol);
+                    else tma_load_2d(dst + kb * kBlock * C::ROW, tm, 0, rows[kb], bar);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < C::HALVES; ++h) {
+                        if constexpr (PAIR) tma_load_2d_hint(dst + h * (kBN * 128) + kb * 2048, tm, 64 * h, rows[kb], bar, pol);
+                        else tma_load_2d(dst + h * (kBN * 128) + kb * 2048, tm, 64 * h, rows[kb], bar);
+                    }
+                }
+            }
+        };
+        const int tmax = max(nA, nB);
+        for (int t = 0; go && t < tmax; ++t) {
+            if (t > 0 && t % 4 == 0) {
+                for (int x = 0; x < 2; ++x) {
+                    cur[x] = nxt[x];
+                    if (x == 0 || nB > 0) nxt[x] = entry(x, (t / 4 + 1) * 32 + lane);
+                }
+            }
+            for (int x = 0; go && x < (shared ? 1 : 2); ++x) {
+                if (t >= (x == 0 ? nA : nB)) continue;
+                const int n = seq(x, t), s = n % ND;
+                int rows[kBlocks];
+#pragma unroll
+                for (int kb = 0; kb < kBlocks; ++kb)
+                    rows[kb] = (__shfl_sync(0xffffffffu, cur[x], (t % 4) * kBlocks + kb) * p.H_kv + g) * kBlock;
+                if (lane == 0 && n >= ND)
+                    go = wait_or_abort(smem_u32(&ke[s]), ((n - ND) / ND) & 1, &s_abort, p.status, p.wait_cycles);
+                go = __shfl_sync(0xffffffffu, go ? 1 : 0, 0);
+                if (!go) break;
+                if (lane == 0) {
+                    if (n == p.hold_tile) mbar_arrive_expect_tx(smem_u32(&kf[s]), BYTES);   // test hook: never lands
+                    else fetch(&tmK, kdst + s * BYTES, rows, smem_u32(&kf[s]));
+                }
+                issued_k = n + 1;
+                if (lane == 0 && n >= ND)
+                    go = wait_or_abort(smem_u32(&ve[s]), ((n - ND) / ND) & 1, &s_abort, p.status, p.wait_cycles);
+                go = __shfl_sync(0xffffffffu, go ? 1 : 0, 0);
+                if (!go) break;
+                if (lane == 0) fetch(&tmV, vdst + s * BYTES, rows, smem_u32(&vf[s]));
+                issued_v = n + 1;
+            }
+        }
+        // Do not leave while copies into this CTA's shared memory may be in flight.  Without an
+        // abort every tile is consumed before the CTA ends.
+        if (lane == 0) {
+            for (int n = max(0, issued_k - ND); n < issued_k; ++n)
+                if (n != p.hold_tile)
+                    mbar_wait_bounded(smem_u32(&kf[n % ND]), (n / ND) & 1, p.wait_cycles);
+            for (int n = max(0, issued_v - ND); n < issued_v; ++n)
+                mbar_wait_bounded(smem_u32(&vf[n % ND]), (n / ND) & 1, p.wait_cycles);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        // The whole warp runs this loop; one elected lane issues each MMA and commit.
+        const uint32_t id_qk = idesc_f16(C::BF16, false, kBM, kBN);
+        const uint32_t id_pv = idesc_f16(C::BF16, true, kBM, D);
+        auto wait = [&](uint64_t& bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, wait_or_abort(smem_u32(&bar), parity, &s_abort, p.status, p.wait_cycles));
+        };
+        auto qk = [&](int x, int s) {
+            const uint32_t kb = sK + s * TILE, qb = sQ + (PAIR ? 0 : x) * TILE;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t off = (ks >> 2) * (kBM * 128) + (ks & 3) * 32;
+                umma_w(tmem + 256 * x, sdesc_k128(qb + off), sdesc_k128(kb + off), id_qk, ks > 0);
+            }
+        };
+        auto pv = [&](int x, int s, int half, bool first) {
+            const uint32_t vb = sV + s * TILE;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int ks = 4 * half + k;
+                umma_ts_w(tmem + 256 * x + 128, tmem + 256 * x + 8 * ks, sdesc_mn128(vb + ks * 2048, kBN * 128), id_pv,
+                          !(first && ks == 0));
+            }
+        };
+        bool ok = true;
+        auto scores = [&](int x, int t) {       // S(x, t), and the release of its K tile after its last reader
+            const int n = seq(x, t), s = n % NS;
+            if (!shared || x == 0) {
+                ok = wait(bars.k_full[s], (n / NS) & 1);
+                if (!ok) return;
+                tc_fence_after();
+            }
+            qk(x, s);
+            umma_commit_w(smem_u32(&bars.s_full[x]));
+            if (!shared || x == 1) umma_commit_w(smem_u32(&bars.k_empty[s]));
+        };
+        scores(0, 0);
+        if (ok && nB > 0) scores(1, 0);
+        for (int t = 0; ok && t < max(nA, nB); ++t) {
+            for (int x = 0; ok && x < 2; ++x) {
+                const int nx = x == 0 ? nA : nB;
+                if (t >= nx) continue;
+                const int n = seq(x, t), s = n % NS;
+                ok = wait(bars.v_full[s], (n / NS) & 1) && wait(bars.p_full[x][0], t & 1);
+                if (!ok) break;
+                tc_fence_after();
+                pv(x, s, 0, t == 0);
+                ok = wait(bars.p_full[x][1], t & 1);
+                if (!ok) break;
+                tc_fence_after();
+                pv(x, s, 1, false);
+                if (!shared || x == 1) umma_commit_w(smem_u32(&bars.v_empty[s]));
+                if (t + 1 < nx) scores(x, t + 1);
+                else umma_commit_w(smem_u32(&bars.o_done[x]));
+            }
+        }
+        // every MMA that was issued, also on an abort, is done before TMEM is freed
+        umma_commit_w(smem_u32(&bars.mma_drain));
+        mbar_wait_bounded(smem_u32(&bars.mma_drain), 0, p.wait_cycles);
+    } else if (warp < 10) {
+        // ------------------------------------------------------------ softmax
+        const int x = (warp - 2) >> 2;
+        const int quarter = warp & 3;                             // the 32 TMEM lanes this warp may touch
+        const int r = quarter * 32 + lane;
+        const int nx = x == 0 ? nA : nB;
+        const int lo = key_lo(x), hi = key_hi(x);
+        const uint32_t tS = tmem + ((uint32_t)(quarter * 32) << 16) + 256 * x;
+        const uint32_t tO = tS + 128;
+        float sl = fabsf(p.scale_log2);
+        float v_unit = 1.f, v_mul = 1.f;
+        if constexpr (C::QUANT) {
+            sl *= s_rowscale[(PAIR ? 0 : x * kBM) + r];
+            const int e = unit_shift(__int_as_float(s_vmax));
+            v_mul = exp2_int(e);
+            v_unit = exp2_int(-e);
+        }
+        float m_used = -INFINITY, l_run = 0.f;
+        bool ok = true;
+        for (int t = 0; t < nx; ++t) {
+            const int n = seq(x, t);
+            ok = __all_sync(0xffffffffu, wait_or_abort(smem_u32(&bars.s_full[x]), t & 1, &s_abort, p.status, p.wait_cycles));
+            if (!ok) break;
+            if constexpr (C::QUANT) {
+                ok = __all_sync(0xffffffffu, wait_or_abort(smem_u32(&bars.sc_full[n % kScaleSlots]), (n / kScaleSlots) & 1,
+                                                           &s_abort, p.status, p.wait_cycles));
+                if (!ok) break;
+            }
+            tc_fence_after();
+            const float2* sc = s_scale + (C::QUANT ? (n % kScaleSlots) * kBlocks : 0);
+            const int left = hi - lo - t * kBN;                   // keys of this tile in the range
+            const bool need_mask = left < kBN;
+            // the row maximum of the tile's scaled scores, 64 at a time
+            float mx = -INFINITY;
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                float v[64];
+                tmem_ld32(tS + 64 * hh, *reinterpret_cast<float(*)[32]>(&v[0]));
+                tmem_ld32(tS + 64 * hh + 32, *reinterpret_cast<float(*)[32]>(&v[32]));
+                tmem_wait_ld();
+                if (need_mask) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j)
+                        if (64 * hh + j >= left) v[j] = -INFINITY;
+                }
+                float m4[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {                     // four paged blocks of 16 keys
+                    float m = fmaxf(v[16 * k], v[16 * k + 1]);
+#pragma unroll
+                    for (int j = 2; j < 16; j += 2) m = fmax3(m, v[16 * k + j], v[16 * k + j + 1]);
+                    // a scale of 0 would turn a masked -inf into NaN: its scores are 0
+                    if constexpr (C::QUANT) m = m == -INFINITY ? m : m * (sl * sc[4 * hh + k].x);
+                    m4[k] = m;
+                }
+                mx = fmax3(mx, fmax3(m4[0], m4[1], m4[2]), m4[3]);
+            }
+            if constexpr (!C::QUANT) mx = mx == -INFINITY ? mx : mx * sl;
+            float m_new = m_used;
+            if (mx > m_used + kSlack || m_used == -INFINITY) m_new = mx;
+            const float alpha = m_used == -INFINITY ? 0.f : ex2(m_used - m_new);
+            const float mref = m_new == -INFINITY ? 0.f : m_new;
+            // the max moved: rescale this row of O (P.V(t-1) is done: s_full(t) says so)
+            if (t > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    tmem_ld32(tO + 32 * c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                    tmem_st32(tO + 32 * c, o);
+                }
+            }
+            // keys past the range: zero their V rows (P is 0 there, V may be stale or NaN).  Tiles
+            // that share V: A's warps, whose P.V runs first.  Converted tiles come zeroed.
+            if (!C::QUANT && need_mask && (!shared || x == 0)) {
+                const int s = n % NS;
+                ok = __all_sync(0xffffffffu, wait_or_abort(smem_u32(&bars.v_full[s]), (n / NS) & 1, &s_abort, p.status, p.wait_cycles));
+                if (!ok) break;
+                const int tid = threadIdx.x - 64 - 128 * x;
+                const int rows = kBN - left;
+                for (int i = tid; i < C::HALVES * rows * 8; i += 128) {
+                    const int c16 = i & 7, rowi = (i >> 3) % rows, half = (i >> 3) / rows;
+                    sts128(sV + s * TILE + half * (kBN * 128) + (left + rowi) * 128 + c16 * 16, 0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+            }
+            // P = 2^(sl S - m) in 16 bits, 32 keys at a time, packed into the tile's first 64 columns
+            // (the scores read from there are no longer needed)
+            const float2 mref2 = make_float2(-mref, -mref);
+            float2 sum2 = make_float2(0.f, 0.f);
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                for (int cc = 0; cc < 2; ++cc) {
+                    const int c = 2 * half + cc;
+                    float v[32];
+                    tmem_ld32(tS + 32 * c, v);
+                    tmem_wait_ld();
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float s1 = sl, vm = 1.f;
+                        if constexpr (C::QUANT) {
+                            const float2 kv = sc[2 * c + (e >> 3)];
+                            s1 = sl * kv.x;
+                            vm = v_mul * kv.y;
+                        }
+                        float2 a = ffma2(make_float2(v[2 * e], v[2 * e + 1]), make_float2(s1, s1), mref2);
+                        if (need_mask) {
+                            if (32 * c + 2 * e >= left) a.x = -INFINITY;
+                            if (32 * c + 2 * e + 1 >= left) a.y = -INFINITY;
+                        }
+                        float2 pp = make_float2(ex2(a.x), ex2(a.y));
+                        sum2 = fadd2(sum2, pp);
+                        if constexpr (C::QUANT) pp = fmul2(pp, make_float2(vm, vm));
+                        w[e] = pack2<C::BF16>(pp.x, pp.y);
+                    }
+                    tmem_st16u(tS + 16 * c, w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[x][half]));
+            }
+            l_run = l_run * alpha + (sum2.x + sum2.y);
+            m_used = m_new;
+        }
+        if (ok && nx > 0 &&
+            __all_sync(0xffffffffu, wait_or_abort(smem_u32(&bars.o_done[x]), 0, &s_abort, p.status, p.wait_cycles))) {
+            tc_fence_after();
+            const int rr = r0 + (PAIR ? 0 : x * kBM) + r;
+            const bool valid = rr < R;
+            const bool final_out = it.whole && nparts == 1;
+            const size_t row = valid ? ragged_row(it, p.G, p.H_q, g, rr) : 0;
+            const size_t slot = ws_slot(p, row, part0 + (PAIR ? x : 0));
+            const float inv = (final_out ? (l_run == 0.f ? 0.f : 1.f / l_run) : 1.f) * v_unit;
+            if (!final_out && valid)
+                st_hint(reinterpret_cast<float2*>(p.ws_ml + slot * 2), make_float2(m_used, l_run), l2_evict_last());
+            __syncwarp();
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                float o[32];
+                tmem_ld32(tO + 32 * c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] *= inv;
+                if (!valid) {
+                } else if (final_out) {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.rg.out16) + row * D + 32 * c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint2 lo2 = pack4(make_float4(o[8 * i], o[8 * i + 1], o[8 * i + 2], o[8 * i + 3]), p.q_bf16);
+                        const uint2 hi2 = pack4(make_float4(o[8 * i + 4], o[8 * i + 5], o[8 * i + 6], o[8 * i + 7]), p.q_bf16);
+                        dst[i] = make_uint4(lo2.x, lo2.y, hi2.x, hi2.y);
+                    }
+                } else {
+                    float4* dst = reinterpret_cast<float4*>(p.ws_o + slot * D + 32 * c);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        st_hint(dst + i, make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]), l2_evict_last());
+                }
+                __syncwarp();                                     // the next TMEM read needs the whole warp
+            }
+        }
+    } else if constexpr (C::QUANT) {
+        // ------------------------------------------------------------ converters
+        // One thread per key of a tile: its row of codes -> its row of the fp16 tile (both
+        // swizzled by 16-byte chunks, so the 32 rows of a warp spread over the banks).
+        const int key = threadIdx.x - 320;                        // 0..127
+        auto convert = [&](uint32_t code, uint32_t dst, bool zero) {
+            const int base = key * C::ROW;
+            const int sw = (base >> 7) & C::SWZ;
+#pragma unroll
+            for (int c = 0; c < C::ROW / 16; ++c) {
+                uint32_t w[4];
+                lds128(w, code + base + ((c ^ sw) << 4));
+                if (zero) w[0] = w[1] = w[2] = w[3] = 0u;
+                if constexpr (DT == PKV_INT4) {                   // 32 elements: 4 chunks of the fp16 row
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t h[4];
+                        codes8_int4(w[i], h);
+                        const int ch = 4 * c + i;
+                        sts128(dst + (ch >> 3) * (kBN * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4), h[0], h[1], h[2], h[3]);
+                    }
+                } else {                                          // 16 elements: 2 chunks
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t h[4];
+                        codes4<DT>(w[2 * i], h[0], h[1]);
+                        codes4<DT>(w[2 * i + 1], h[2], h[3]);
+                        const int ch = 2 * c + i;
+                        sts128(dst + (ch >> 3) * (kBN * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4), h[0], h[1], h[2], h[3]);
+                    }
+                }
+            }
+        };
+        auto wait = [&](uint64_t& bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, wait_or_abort(smem_u32(&bar), parity, &s_abort, p.status, p.wait_cycles));
+        };
+        auto scales_of = [&](int x, int t) {                      // threads 0..7: one block of the tile each
+            const int k = key_lo(x) + t * kBN + key * kBlock;
+            if (key >= kBlocks || k >= key_hi(x)) return make_float2(0.f, 0.f);
+            const size_t i = (size_t)block_id(k / kBlock) * p.H_kv + g;
+            return make_float2(p.k_scale[i], p.v_scale[i]);
+        };
+        bool ok = true;
+        const int tmax = max(nA, nB);
+        float2 next[2] = {scales_of(0, 0), nB > 0 ? scales_of(1, 0) : make_float2(0.f, 0.f)};
+        for (int t = 0; ok && t < tmax; ++t) {
+            for (int x = 0; ok && x < (shared ? 1 : 2); ++x) {
+                const int nx = x == 0 ? nA : nB;
+                if (t >= nx) continue;
+                const int n = seq(x, t), s = n % NS, cs = n % NC;
+                const float2 mine = next[x];
+                if (t + 1 < nx) next[x] = scales_of(x, t + 1);
+                const int left = key_hi(x) - key_lo(x) - t * kBN;
+                ok = wait(bars.ck_full[cs], (n / NC) & 1) && (n < NS || wait(bars.k_empty[s], ((n - NS) / NS) & 1));
+                if (!ok) break;
+                if (key < kBlocks) s_scale[(n % kScaleSlots) * kBlocks + key] = mine;
+                convert(sCK + cs * C::CTILE, sK + s * TILE, false);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&bars.sc_full[n % kScaleSlots]));
+                    mbar_arrive(smem_u32(&bars.k_full[s]));
+                    mbar_arrive(smem_u32(&bars.ck_empty[cs]));
+                }
+                ok = wait(bars.cv_full[cs], (n / NC) & 1) && (n < NS || wait(bars.v_empty[s], ((n - NS) / NS) & 1));
+                if (!ok) break;
+                convert(sCV + cs * C::CTILE, sV + s * TILE, key >= left);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&bars.v_full[s]));
+                    mbar_arrive(smem_u32(&bars.cv_empty[cs]));
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) {
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+template <int D, int DT, bool PAIR>
+int launch(const DecodeParams& p, int items, int max_rows, const CUtensorMap* tmk, const CUtensorMap* tmv, cudaStream_t s)
+{
+    using C = Cfg<D, DT, PAIR>;
+    auto kern = ragged_tc_kernel<D, DT, PAIR>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    const int zparts = PAIR ? (p.max_parts + 1) / 2 : p.max_parts;
+    const dim3 grid((max_rows * p.G + C::QT * kBM - 1) / (C::QT * kBM), p.H_kv, items * zparts);
+    kern<<<grid, C::THREADS, C::SMEM, s>>>(p, *tmk, *tmv);
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+template <int DT>
+int launch_any(const DecodeParams& p, int d, bool pair, int items, int max_rows, const CUtensorMap* tmk,
+               const CUtensorMap* tmv, cudaStream_t s)
+{
+    if (d == 128) return pair ? launch<128, DT, true>(p, items, max_rows, tmk, tmv, s)
+                              : launch<128, DT, false>(p, items, max_rows, tmk, tmv, s);
+    return pair ? launch<64, DT, true>(p, items, max_rows, tmk, tmv, s)
+                : launch<64, DT, false>(p, items, max_rows, tmk, tmv, s);
+}
+
+}  // namespace ragged
+
+}  // namespace pkv

@@ -1,0 +1,12 @@
+// ragged_tc_f16.cu -- the tcgen05 kernel of the ragged operators for f16 pools (ragged_tc.cuh).
+#include "ragged_tc.cuh"
+
+namespace pkv {
+
+int launch_ragged_tc_f16(const DecodeParams& p, int d, bool pair, int items, int max_rows, const CUtensorMap* tmk,
+                      const CUtensorMap* tmv, cudaStream_t s)
+{
+    return ragged::launch_any<PKV_F16>(p, d, pair, items, max_rows, tmk, tmv, s);
+}
+
+}  // namespace pkv

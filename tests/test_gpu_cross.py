@@ -134,14 +134,18 @@ def test_cross_reports_and_clips():
     assert torch.equal(out[:4], good[:4]) and (out[4:34] == 0).all() and torch.equal(out[34:], good[34:])
     out, status = call(st, torch.tensor([100, 300, 100000], dtype=torch.int32))
     assert status & pkv.DEV_BAD_LENGTH and torch.equal(out[:34], good[:34])
+    # bounds choose the kernel, so other bounds give other roundings: within the tolerance of the oracle
+    ref = reference(opool, q, qd, tables, ctx, [0] * 4 + [1] * 30 + [2] * 2, 0.1)
+    tol = tolerance(opool, q, ref, ctx, 0.1, True)
+    check(good, ref, tol)
     out, status = call(st, cl, mr=10)
-    assert status == pkv.DEV_BAD_LENGTH
-    assert torch.equal(out[:4], good[:4]) and (out[14:34] == 9).all()
-    torch.testing.assert_close(out[4:14].float(), good[4:14].float(), atol=0.02, rtol=0.02)
+    assert status == pkv.DEV_BAD_LENGTH and (out[14:34] == 9).all()
+    for rows_ in (slice(0, 14), slice(34, 36)):
+        check(out[rows_], ref[rows_], tol[rows_])
     bad = torch.tensor([0, 4, 2, 5000], dtype=torch.int32)       # descending, then past the end
     out, status = call(bad, cl)
     assert status == pkv.DEV_BAD_LENGTH
-    torch.testing.assert_close(out[:2].float(), good[:2].float(), atol=0.02, rtol=0.02)
+    check(out[:2], ref[:2], tol[:2])
     tb = tables.clone()
     tb[2, 1] = 10 ** 6
     out, status = call(st, cl, tb=tb)

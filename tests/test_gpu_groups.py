@@ -55,6 +55,8 @@ SHAPES = [
     (12, 4, [5, 1], [300 * 16, 16], [40, 1, 500, 0, 3, 129]),              # 3 heads per KV head, split prefix
     (64, 8, [20, 9], [1024, 400], drawn(1, 29, 0, 90)),                    # the 70B head shape
     (16, 1, [40], [272], drawn(2, 40, 0, 40)),                            # one KV head, 640 rows
+    (64, 1, [3, 2], [512, 32], [130, 0, 1, 17, 300]),                      # MQA: 64 rows per sequence
+    (96, 1, [2], [160], [200, 5]),                                         # 96 heads on one KV head
 ]
 
 
