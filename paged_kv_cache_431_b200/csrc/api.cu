@@ -81,6 +81,45 @@ static bool make_map(CUtensorMap* map, void* base, const pkv_pool_desc& d, int r
     return r == CUDA_SUCCESS;
 }
 
+// One layer's 16-bit K or V pool as [8-row groups][halves of 64 dims][8 rows][64 dims], so that a
+// paged block (two 8-row groups) is one box whose shared-memory image is two groups in a row.
+static bool make_block_map(CUtensorMap* map, void* base, const pkv_pool_desc& d)
+{
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t row = (cuuint64_t)d.head_dim * 2;
+    const cuuint64_t dims[4] = {64, 8, (cuuint64_t)d.head_dim / 64, (cuuint64_t)d.num_blocks * d.num_kv_heads * 2};
+    const cuuint64_t strides[3] = {row, 128, 8 * row};
+    const cuuint32_t box[4] = {64, 8, (cuuint32_t)d.head_dim / 64, 2};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int layer_block_maps(pkv_pool* pool, int layer, const CUtensorMap** tmk, const CUtensorMap** tmv)
+{
+    std::lock_guard<std::mutex> lock(pool->mu);
+    if (pool->tmk4.empty()) {
+        const int L = pool->d.num_layers;
+        std::vector<CUtensorMap> k, v;
+        try {
+            k.resize(L);
+            v.resize(L);
+        } catch (...) {
+            return PKV_ERR_CUDA;
+        }
+        for (int l = 0; l < L; ++l)
+            if (!make_block_map(&k[l], pool->k_base[l], pool->d) || !make_block_map(&v[l], pool->v_base[l], pool->d))
+                return PKV_ERR_CUDA;
+        pool->tmk4.swap(k);
+        pool->tmv4.swap(v);
+    }
+    *tmk = &pool->tmk4[layer];
+    *tmv = &pool->tmv4[layer];
+    return PKV_OK;
+}
+
 int layer_maps(pkv_pool* pool, int layer, const CUtensorMap** tmk, const CUtensorMap** tmv)
 {
     std::lock_guard<std::mutex> lock(pool->mu);
@@ -663,11 +702,13 @@ static RaggedSplit ragged_split(pkv_pool_t pool, int items, int max_rows, int G,
     return r;
 }
 
-static int launch_ragged(const RaggedArgs& a, const RaggedSplit& sp, const CUtensorMap* tmk, const CUtensorMap* tmv,
-                         cudaStream_t s)
+static int launch_ragged(pkv_pool_t pool, int layer, const RaggedArgs& a, const RaggedSplit& sp, cudaStream_t s)
 {
-    if (!sp.tc) return launch_ragged_short(a, tmk, tmv, s);
-    return launch_ragged_tc(a, sp.pair, tmk, tmv, s);
+    const CUtensorMap *tmk = nullptr, *tmv = nullptr;
+    const bool blocks = sp.tc && !is_quantized(a.kv_dtype);
+    const int rc = blocks ? layer_block_maps(pool, layer, &tmk, &tmv) : layer_maps(pool, layer, &tmk, &tmv);
+    if (rc != PKV_OK) return rc;
+    return sp.tc ? launch_ragged_tc(a, sp.pair, tmk, tmv, s) : launch_ragged_short(a, tmk, tmv, s);
 }
 
 static size_t ragged_ws_bytes(pkv_pool_t pool, int rows, int num_q_heads, int slots)
@@ -753,9 +794,6 @@ int paged_cross_attn(pkv_pool_t pool, int layer, const void* q, int q_dtype, con
     const size_t need = sp.parts > 1 ? ragged_ws_bytes(pool, total_rows, num_q_heads, sp.parts) : 0;
     if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15)))
         return PKV_ERR_WORKSPACE;
-    const CUtensorMap *tmk = nullptr, *tmv = nullptr;
-    rc = layer_maps(pool, layer, &tmk, &tmv);
-    if (rc != PKV_OK) return rc;
     a.mode = 0;   // kCross
     a.items = a.starts = num_seqs;
     a.max_rows = max_rows;
@@ -764,7 +802,7 @@ int paged_cross_attn(pkv_pool_t pool, int layer, const void* q, int q_dtype, con
     a.ws_o = need ? static_cast<float*>(workspace) : nullptr;
     a.ws_ml = need ? a.ws_o + (size_t)total_rows * num_q_heads * sp.parts * a.d : nullptr;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    rc = launch_ragged(a, sp, tmk, tmv, s);
+    rc = launch_ragged(pool, layer, a, sp, s);
     if (rc != PKV_OK || sp.parts <= 1) return rc;
     return launch_ragged_merge(a, s);
 }
@@ -805,12 +843,10 @@ int paged_decode_attn_groups(pkv_pool_t pool, int layer, const void* q, int q_dt
     const size_t need = slots > 1 ? ragged_ws_bytes(pool, num_seqs, num_q_heads, slots) : 0;
     if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15)))
         return PKV_ERR_WORKSPACE;
-    const CUtensorMap *tmk = nullptr, *tmv = nullptr;
-    rc = layer_maps(pool, layer, &tmk, &tmv);
-    if (rc != PKV_OK) return rc;
     a.starts = num_groups;
     a.prefix_lens = prefix_lens;
     a.max_prefix = max_prefix_len;
+    a.max_group = max_group_size;
     a.slots = slots;
     a.ws_o = need ? static_cast<float*>(workspace) : nullptr;
     a.ws_ml = need ? a.ws_o + (size_t)num_seqs * num_q_heads * slots * a.d : nullptr;
@@ -822,7 +858,7 @@ int paged_decode_attn_groups(pkv_pool_t pool, int layer, const void* q, int q_dt
         a.max_rows = max_group_size;
         a.part_tokens = pre.part;
         a.max_parts = pre.parts;
-        rc = launch_ragged(a, pre, tmk, tmv, s);
+        rc = launch_ragged(pool, layer, a, pre, s);
         if (rc != PKV_OK) return rc;
     }
     // 2. every sequence's own tokens, 3. the merge of both
@@ -833,7 +869,7 @@ int paged_decode_attn_groups(pkv_pool_t pool, int layer, const void* q, int q_dt
     a.max_parts = own.parts;
     a.part_base = pre.parts;
     a.pre_part = pre.part;
-    rc = launch_ragged(a, own, tmk, tmv, s);
+    rc = launch_ragged(pool, layer, a, own, s);
     if (rc != PKV_OK || slots <= 1) return rc;
     return launch_ragged_merge(a, s);
 }

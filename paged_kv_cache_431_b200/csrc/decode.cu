@@ -515,10 +515,10 @@ __global__ void __launch_bounds__(32 * kMergeHeads) ragged_merge_kernel(const De
     const int h = (blockIdx.x % per_row) * kMergeHeads + (threadIdx.x >> 5);
     const RaggedParams& r = p.rg;
     const int item = item_of_row(r, t);
-    if (item < 0 || h >= p.H_q) return;
-    int pre = 0, own;      // partials of the prefix, of the rest
+    int pre = 0, own = 0;  // partials of the prefix, of the rest
     bool whole = true;
-    if (r.mode == kSuffix) {
+    if (item < 0 || h >= p.H_q) {
+    } else if (r.mode == kSuffix) {
         const RaggedItem it = ragged_item(r, p.ctx_lens, p.W, p.max_parts * p.part_tokens, t, p.status, false);
         pre = (it.base + r.pre_part - 1) / r.pre_part;
         own = (it.end - it.base + p.part_tokens - 1) / p.part_tokens;
@@ -533,13 +533,12 @@ __global__ void __launch_bounds__(32 * kMergeHeads) ragged_merge_kernel(const De
     } else {
         int row0, rows;
         item_rows(r, item, row0, rows, p.status, false);
-        if (t >= row0 + rows) return;            // beyond what the grid covered
         const RaggedItem it = ragged_item(r, p.ctx_lens, p.W, p.max_parts * p.part_tokens, item, p.status, false);
-        own = (it.end + p.part_tokens - 1) / p.part_tokens;
+        if (t < row0 + rows) own = (it.end + p.part_tokens - 1) / p.part_tokens;   // else: beyond the grid
     }
     pdl_wait_primary();   // the partials of the kernels before this one
     const int n = pre + own;
-    if (whole && n <= 1) return;
+    if (whole && n <= 1) return;   // written whole, padding, or not covered
     const size_t row = (size_t)t * p.H_q + h;
     const size_t base = row * p.slots;
     const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + base;
@@ -792,7 +791,7 @@ static DecodeParams ragged_params(const RaggedArgs& a)
     p.rg.max_rows = a.max_rows;
     p.rg.max_prefix = a.max_prefix;
     p.rg.pre_part = a.pre_part;
-    p.rg.pre_slots = a.part_base;
+    p.rg.max_group = a.max_group;
     p.rg.out16 = a.out;
     return p;
 }

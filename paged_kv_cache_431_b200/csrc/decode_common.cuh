@@ -35,7 +35,8 @@ struct RaggedParams {
     int items;                    // row_starts has items + 1 entries
     int total_rows, max_rows;     // rows of q; rows of an item that the grid covers
     int max_prefix;               // kPrefix, kSuffix: tokens of a prefix that the grid covers
-    int pre_part, pre_slots;      // kSuffix and its merge: tokens per prefix partition, workspace slots before the suffix's
+    int pre_part;                 // kSuffix's merge: tokens per prefix partition
+    int max_group;                // kSuffix: sequences of a group that the prefix pass covered
     void* out16;                  // [total_rows][H_q][d] of q's dtype
 };
 
@@ -156,9 +157,11 @@ __device__ __forceinline__ RaggedItem ragged_item(const RaggedParams& r, const i
     RaggedItem it;
     it.base = 0;
     if (r.mode == kSuffix) {
-        const int g = item_of_row(r, b);
+        // a sequence of no group is padding; one past max_group was not covered (and was reported)
+        int g = item_of_row(r, b);
+        if (g >= 0 && b - r.row_starts[g] >= r.max_group) g = -1;
         it.row0 = it.table = b;
-        it.rows = g >= 0 ? 1 : 0;                // a sequence behind the last group is padding
+        it.rows = g >= 0 ? 1 : 0;
         it.end = g >= 0 ? ctx_lens[b] : 0;
         it.base = g >= 0 ? group_prefix(r, W, g, status, report) : 0;
         it.whole = it.base == 0;

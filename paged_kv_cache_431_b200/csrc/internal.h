@@ -23,6 +23,7 @@ struct pkv_pool {
     std::mutex mu;             // guards the lazily built tensor maps
     bool maps_ready = false;
     std::vector<CUtensorMap> tmk, tmv;   // per layer: K and V pool as a 2-D tensor
+    std::vector<CUtensorMap> tmk4, tmv4;   // 16-bit pools: as (64 dims, 8 rows, halves, 8-row groups)
 };
 
 namespace pkv {
@@ -41,6 +42,9 @@ bool is_quantized(int dtype);
 
 // Tensor maps for `layer` (built on first use). Returns PKV_OK or PKV_ERR_CUDA.
 int layer_maps(pkv_pool* pool, int layer, const CUtensorMap** tmk, const CUtensorMap** tmv);
+
+// The 4-D maps of a 16-bit pool's layer (one paged block = one box), built with the others.
+int layer_block_maps(pkv_pool* pool, int layer, const CUtensorMap** tmk, const CUtensorMap** tmv);
 
 int num_sms();
 
@@ -143,7 +147,7 @@ struct RaggedArgs {
     int H_q, H_kv, G, N, d, kv_dtype;
     int part_tokens, max_parts;
     int part_base, slots;   // first workspace slot of this launch, slots per row
-    int max_prefix, pre_part;
+    int max_prefix, pre_part, max_group;
     float scale;
     const float* k_scale;
     const float* v_scale;

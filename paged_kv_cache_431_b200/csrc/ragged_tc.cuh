@@ -4,15 +4,15 @@
 // with R = rows x G query rows per KV head this is a dense [R x keys] contraction:
 //   S = Q.K^T,  P = 2^(scale S - m),  O += P.V,  out = O / sum P
 // One CTA (one per SM) holds two query tiles A and B of 128 rows in flight, so that the tensor
-// cores work on one while the softmax warps work on the other:
+// cores work on one while the softmax warps work on the other (one warp issues the MMAs of each):
 //   !PAIR  A and B are 256 consecutive rows that share every K/V tile (bound by the tensor cores
 //          and by the exponentials: 2 x 128 x 128 of them per key tile on 16 lanes a cycle are as
 //          many cycles as the four MMAs);
 //   PAIR   (at most 128 rows per item and KV head: bound by the K/V bytes) A and B are the SAME
 //          rows against two key partitions, each with its own K/V tiles; both write partials.
-// Warps: 0 fetches (TMA, one box per paged block and 64 dims), 1 issues every MMA, 2..5 and 6..9
-// are the softmax of A and B (one thread per query row = TMEM lane); for quantized pools 10..13
-// turn fetched code tiles into fp16 tiles (the codes are exact in fp16; the K scale of a (block,
+// Warps: 0..3 and 4..7 are the softmax of A and B (one thread per query row = TMEM lane), 8 and 10
+// fetch K and V (TMA, one box per paged block), 9 and 11 issue the MMAs of A and B; for quantized pools
+// 12..15 turn fetched code tiles into fp16 tiles (the codes are exact in fp16; the K scale of a (block,
 // head) multiplies its 16 scores, its V scale multiplies P, so a tile is converted once for all
 // rows).  Per key tile and query tile: S (128 columns of TMEM) -> P back over the same columns as
 // 16-bit pairs, the A operand of P.V, in two halves of 64 keys so that P.V starts while the other
@@ -29,6 +29,8 @@
 
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "decode_common.cuh"
 #include "tcgen05.cuh"
 
@@ -41,6 +43,10 @@ constexpr int kBN = 128;                         // keys per tile
 constexpr int kBlocks = kBN / kBlock;            // paged blocks per key tile
 constexpr float kSlack = 8.f;                    // log2 units the running max may lag
 constexpr uint32_t kTmemCols = 512;              // tile x: S and P at 256x, O at 256x + 128
+#ifndef PKV_POLY_EVERY
+#define PKV_POLY_EVERY 4
+#endif
+constexpr int kPolyEvery = PKV_POLY_EVERY;       // of so many pairs of exponentials, one is a polynomial
 constexpr int kScaleSlots = 4;                   // key tiles whose scales are kept
 
 template <int D, int DT, bool PAIR>
@@ -56,9 +62,22 @@ struct Cfg {
     static constexpr int NS = QUANT ? 2 : (D == 64 ? 4 : PAIR ? 3 : 2);
     static constexpr int NC = QUANT ? (PAIR || D == 64 ? 2 : DT == PKV_INT4 ? 2 : 1) : 1;
     static constexpr int SMEM = QT * TILE + NS * 2 * TILE + NC * 2 * CTILE + 1024;
-    static constexpr int THREADS = QUANT ? 448 : 320;
+    static constexpr int THREADS = QUANT ? 512 : 384;
+    // registers of a softmax thread: a row's 128 scores stay in them.  The block is launched with
+    // THREADS x 168 (quantized: 128) and gives what the other warpgroups release: 2 x 216 + 72 =
+    // 3 x 168; 2 x 168 + 72 + 96 <= 4 x 128.
+    static constexpr int SOFTMAX_REGS = QUANT ? 168 : 216;
     static constexpr int SWZ = ROW >= 128 ? 7 : ROW == 64 ? 3 : 1;   // TMA swizzle of a code tile
     static_assert(SMEM <= 225 * 1024, "dynamic shared memory, with 2 KB left for the static part");
+};
+
+// K or V tile layout, 16 bits: 8-row groups; within one, the 64-dim halves; within those 8 rows of
+// 128 bytes (128-byte swizzle).  A paged block of 16 rows is two groups, so it is ONE box of a 4-D
+// view of the pool (64 dims, 8 rows, halves, 8-row groups).
+template <int D>
+struct KV {
+    static constexpr int GROUP = 8 * D * 2;          // bytes of an 8-row group
+    static constexpr int HALF = 1024;                // between the halves of a group
 };
 
 struct Bars {
@@ -68,7 +87,7 @@ struct Bars {
     uint64_t s_full[2];        // S(x, t) is in TMEM, and every earlier MMA of the CTA is done
     uint64_t p_full[2][2];     // a half of P(x, t) is stored
     uint64_t o_done[2];
-    uint64_t mma_drain;
+    uint64_t mma_drain[2];
 };
 
 __device__ __forceinline__ float2 fmul2(float2 a, float2 b)
@@ -76,6 +95,44 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b)
     unsigned long long d;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2bits(a)), "l"(f2bits(b)));
     return bitsf2(d);
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// 2^a for a pair, on the FMA pipe: a = n + f with n the nearest integer (by adding 1.5 x 2^23), 2^f
+// on [-1/2, 1/2] by the minimax polynomial of degree 3 (relative error 2^-13.7, against the half
+// step 2^-9 of a bf16 P) or 4 (2^-18.5, against 2^-12), n added to the exponent field.  a is at most
+// kSlack; below -126 it counts as -126.
+template <int DEG>
+__device__ __forceinline__ float2 exp2_poly(float2 a)
+{
+    constexpr float M = 12582912.f;
+    a = make_float2(fmaxf(a.x, -126.f), fmaxf(a.y, -126.f));
+    const float2 t = fadd2(a, make_float2(M, M));
+    const float2 f = fsub2(a, fsub2(t, make_float2(M, M)));
+    auto c2 = [](float c) { return make_float2(c, c); };
+    float2 y;
+    if constexpr (DEG == 3) {
+        y = ffma2(c2(0x1.c3f760p-5f), f, c2(0x1.f0de1ap-3f));
+        y = ffma2(y, f, c2(0x1.62f31ap-1f));
+        y = ffma2(y, f, c2(0x1.fff692p-1f));
+    } else {
+        y = ffma2(c2(0x1.3997d6p-7f), f, c2(0x1.ca1440p-5f));
+        y = ffma2(y, f, c2(0x1.ec06dap-3f));
+        y = ffma2(y, f, c2(0x1.62e0dcp-1f));
+        y = ffma2(y, f, c2(0x1.ffffe8p-1f));
+    }
+    return make_float2(__int_as_float(__float_as_int(y.x) + (__float_as_int(t.x) << 23)),
+                       __int_as_float(__float_as_int(y.y) + (__float_as_int(t.y) << 23)));
 }
 
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((127 + e) << 23); }   // e in [-126, 127]
@@ -142,6 +199,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
     __shared__ float s_rowscale[C::QUANT ? C::QT * kBM : 1];              // per query row: 2^-e of its fp16 q
     __shared__ __align__(8) float2 s_scale[C::QUANT ? kScaleSlots * kBlocks : 1];   // (K, V) scales of a key tile's blocks
     __shared__ int s_vmax;
+    __shared__ volatile int s_armed[2];                           // K, V tiles whose full barrier is in their phase
 
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -175,7 +233,6 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
         return max(0, (key_hi(x) - key_lo(x) + kBN - 1) / kBN);
     };
     const int nA = ntiles(0), nB = ntiles(1);
-    const int nseq = shared ? nA : nA + nB;                       // K/V tiles of this CTA
     auto seq = [&](int x, int t) { return shared ? t : x == 0 ? t + min(t, nB) : t + min(t + 1, nA); };
 
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
@@ -188,11 +245,12 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
     if (threadIdx.x == 0) {
         s_abort = 0;
         s_vmax = 0;
+        s_armed[0] = s_armed[1] = 0;
         for (int s = 0; s < NS; ++s) {
             mbar_init(smem_u32(&bars.k_full[s]), C::QUANT ? 4 : 1);
-            mbar_init(smem_u32(&bars.k_empty[s]), 1);
+            mbar_init(smem_u32(&bars.k_empty[s]), shared ? 2 : 1);
             mbar_init(smem_u32(&bars.v_full[s]), C::QUANT ? 4 : 1);
-            mbar_init(smem_u32(&bars.v_empty[s]), 1);
+            mbar_init(smem_u32(&bars.v_empty[s]), shared ? 2 : 1);
         }
         if constexpr (C::QUANT) {
             for (int s = 0; s < NC; ++s) {
@@ -209,12 +267,12 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
             mbar_init(smem_u32(&bars.p_full[x][1]), 4);
             mbar_init(smem_u32(&bars.o_done[x]), 1);
         }
-        mbar_init(smem_u32(&bars.mma_drain), 1);
+        for (int x = 0; x < 2; ++x) mbar_init(smem_u32(&bars.mma_drain[x]), 1);
         mbar_fence_init();
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
     }
-    if (warp == 1) {
+    if (warp == 9) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem_base)),
                      "r"(kTmemCols)
                      : "memory");
@@ -284,150 +342,39 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
     tc_fence_after();
     const uint32_t tmem = s_tmem_base;
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ producer
-        // The lanes hold the block ids of the next 4 key tiles of A and of B (one load per 4 tiles,
-        // a chunk ahead); lane 0 issues the copies.  Keys past the range fetch block 0: in bounds,
-        // masked, and their V rows zeroed.
-        int cur[2], nxt[2];
-        auto entry = [&](int x, int i) -> int {
-            const int lb = key_lo(x) / kBlock + i;
-            return lb * kBlock < key_hi(x) ? block_id(lb) : 0;
-        };
-        for (int x = 0; x < 2; ++x) {
-            cur[x] = (x == 0 || nB > 0) ? entry(x, lane) : 0;
-            nxt[x] = (x == 0 || nB > 0) ? entry(x, 32 + lane) : 0;
-        }
-        constexpr int ND = C::QUANT ? NC : NS;                    // depth of the rings the copies go to
-        uint64_t* kf = C::QUANT ? bars.ck_full : bars.k_full;
-        uint64_t* ke = C::QUANT ? bars.ck_empty : bars.k_empty;
-        uint64_t* vf = C::QUANT ? bars.cv_full : bars.v_full;
-        uint64_t* ve = C::QUANT ? bars.cv_empty : bars.v_empty;
-        constexpr uint32_t BYTES = C::QUANT ? C::CTILE : TILE;
-        const uint32_t kdst = C::QUANT ? sCK : sK, vdst = C::QUANT ? sCV : sV;
-        int issued_k = 0, issued_v = 0;
-        bool go = true;
-        const uint64_t pol = l2_evict_first();
-        auto fetch = [&](const CUtensorMap* tm, uint32_t dst, const int (&rows)[kBlocks], uint32_t bar) {
-            mbar_arrive_expect_tx(bar, BYTES);
-#pragma unroll
-            for (int kb = 0; kb < kBlocks; ++kb) {
-                if constexpr (C::QUANT) {
-                    if constexpr (PAIR) tma_load_2d_hint(dst + kb * kBlock * C::ROW, tm, 0, rows[kb], bar, pol);
-                    else tma_load_2d(dst + kb * kBlock * C::ROW, tm, 0, rows[kb], bar);
-                } else {
-#pragma unroll
-                    for (int h = 0; h < C::HALVES; ++h) {
-                        if constexpr (PAIR) tma_load_2d_hint(dst + h * (kBN * 128) + kb * 2048, tm, 64 * h, rows[kb], bar, pol);
-                        else tma_load_2d(dst + h * (kBN * 128) + kb * 2048, tm, 64 * h, rows[kb], bar);
+    // A wait of a whole warp: agreed on by its lanes; the abort flag is looked at only where the
+    // barrier is not there yet.
+    auto wait = [&](uint64_t& bar, uint32_t parity) {
+        const bool there = mbar_try_wait(smem_u32(&bar), parity);
+        if (__all_sync(0xffffffffu, there)) return true;
+        return (bool)__all_sync(0xffffffffu, wait_or_abort(smem_u32(&bar), parity, &s_abort, p.status, p.wait_cycles));
+    };
+
+    // Waits for K (V) tile n in the ring.  In the PAIR form A and B take turns on the stages but run
+    // at their own pace, and a barrier's parity cannot tell tile n's phase from the one two before:
+    // so the wait on it starts only once tile n is armed, which its fetcher does after the stage's
+    // previous tile was consumed.
+    auto wait_tile = [&](int which, uint64_t* full, int n) {
+        if constexpr (PAIR) {
+            if (s_armed[which] <= n) {
+                const long long t0 = clock64();
+                while (s_armed[which] <= n) {
+                    if (s_abort) break;
+                    if (clock64() - t0 > p.wait_cycles) {
+                        s_abort = 1;
+                        flag_status(p.status, PKV_DEV_TIMEOUT);
                     }
                 }
             }
-        };
-        const int tmax = max(nA, nB);
-        for (int t = 0; go && t < tmax; ++t) {
-            if (t > 0 && t % 4 == 0) {
-                for (int x = 0; x < 2; ++x) {
-                    cur[x] = nxt[x];
-                    if (x == 0 || nB > 0) nxt[x] = entry(x, (t / 4 + 1) * 32 + lane);
-                }
-            }
-            for (int x = 0; go && x < (shared ? 1 : 2); ++x) {
-                if (t >= (x == 0 ? nA : nB)) continue;
-                const int n = seq(x, t), s = n % ND;
-                int rows[kBlocks];
-#pragma unroll
-                for (int kb = 0; kb < kBlocks; ++kb)
-                    rows[kb] = (__shfl_sync(0xffffffffu, cur[x], (t % 4) * kBlocks + kb) * p.H_kv + g) * kBlock;
-                if (lane == 0 && n >= ND)
-                    go = wait_or_abort(smem_u32(&ke[s]), ((n - ND) / ND) & 1, &s_abort, p.status, p.wait_cycles);
-                go = __shfl_sync(0xffffffffu, go ? 1 : 0, 0);
-                if (!go) break;
-                if (lane == 0) {
-                    if (n == p.hold_tile) mbar_arrive_expect_tx(smem_u32(&kf[s]), BYTES);   // test hook: never lands
-                    else fetch(&tmK, kdst + s * BYTES, rows, smem_u32(&kf[s]));
-                }
-                issued_k = n + 1;
-                if (lane == 0 && n >= ND)
-                    go = wait_or_abort(smem_u32(&ve[s]), ((n - ND) / ND) & 1, &s_abort, p.status, p.wait_cycles);
-                go = __shfl_sync(0xffffffffu, go ? 1 : 0, 0);
-                if (!go) break;
-                if (lane == 0) fetch(&tmV, vdst + s * BYTES, rows, smem_u32(&vf[s]));
-                issued_v = n + 1;
-            }
+            if (!__all_sync(0xffffffffu, s_armed[which] > n)) return false;
         }
-        // Do not leave while copies into this CTA's shared memory may be in flight.  Without an
-        // abort every tile is consumed before the CTA ends.
-        if (lane == 0) {
-            for (int n = max(0, issued_k - ND); n < issued_k; ++n)
-                if (n != p.hold_tile)
-                    mbar_wait_bounded(smem_u32(&kf[n % ND]), (n / ND) & 1, p.wait_cycles);
-            for (int n = max(0, issued_v - ND); n < issued_v; ++n)
-                mbar_wait_bounded(smem_u32(&vf[n % ND]), (n / ND) & 1, p.wait_cycles);
-        }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        // The whole warp runs this loop; one elected lane issues each MMA and commit.
-        const uint32_t id_qk = idesc_f16(C::BF16, false, kBM, kBN);
-        const uint32_t id_pv = idesc_f16(C::BF16, true, kBM, D);
-        auto wait = [&](uint64_t& bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, wait_or_abort(smem_u32(&bar), parity, &s_abort, p.status, p.wait_cycles));
-        };
-        auto qk = [&](int x, int s) {
-            const uint32_t kb = sK + s * TILE, qb = sQ + (PAIR ? 0 : x) * TILE;
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t off = (ks >> 2) * (kBM * 128) + (ks & 3) * 32;
-                umma_w(tmem + 256 * x, sdesc_k128(qb + off), sdesc_k128(kb + off), id_qk, ks > 0);
-            }
-        };
-        auto pv = [&](int x, int s, int half, bool first) {
-            const uint32_t vb = sV + s * TILE;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int ks = 4 * half + k;
-                umma_ts_w(tmem + 256 * x + 128, tmem + 256 * x + 8 * ks, sdesc_mn128(vb + ks * 2048, kBN * 128), id_pv,
-                          !(first && ks == 0));
-            }
-        };
-        bool ok = true;
-        auto scores = [&](int x, int t) {       // S(x, t), and the release of its K tile after its last reader
-            const int n = seq(x, t), s = n % NS;
-            if (!shared || x == 0) {
-                ok = wait(bars.k_full[s], (n / NS) & 1);
-                if (!ok) return;
-                tc_fence_after();
-            }
-            qk(x, s);
-            umma_commit_w(smem_u32(&bars.s_full[x]));
-            if (!shared || x == 1) umma_commit_w(smem_u32(&bars.k_empty[s]));
-        };
-        scores(0, 0);
-        if (ok && nB > 0) scores(1, 0);
-        for (int t = 0; ok && t < max(nA, nB); ++t) {
-            for (int x = 0; ok && x < 2; ++x) {
-                const int nx = x == 0 ? nA : nB;
-                if (t >= nx) continue;
-                const int n = seq(x, t), s = n % NS;
-                ok = wait(bars.v_full[s], (n / NS) & 1) && wait(bars.p_full[x][0], t & 1);
-                if (!ok) break;
-                tc_fence_after();
-                pv(x, s, 0, t == 0);
-                ok = wait(bars.p_full[x][1], t & 1);
-                if (!ok) break;
-                tc_fence_after();
-                pv(x, s, 1, false);
-                if (!shared || x == 1) umma_commit_w(smem_u32(&bars.v_empty[s]));
-                if (t + 1 < nx) scores(x, t + 1);
-                else umma_commit_w(smem_u32(&bars.o_done[x]));
-            }
-        }
-        // every MMA that was issued, also on an abort, is done before TMEM is freed
-        umma_commit_w(smem_u32(&bars.mma_drain));
-        mbar_wait_bounded(smem_u32(&bars.mma_drain), 0, p.wait_cycles);
-    } else if (warp < 10) {
+        return wait(full[n % NS], (n / NS) & 1);
+    };
+
+    if (warp < 8) {
         // ------------------------------------------------------------ softmax
-        const int x = (warp - 2) >> 2;
+        regs_inc<C::SOFTMAX_REGS>();
+        const int x = warp >> 2;
         const int quarter = warp & 3;                             // the 32 TMEM lanes this warp may touch
         const int r = quarter * 32 + lane;
         const int nx = x == 0 ? nA : nB;
@@ -446,42 +393,43 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
         bool ok = true;
         for (int t = 0; t < nx; ++t) {
             const int n = seq(x, t);
-            ok = __all_sync(0xffffffffu, wait_or_abort(smem_u32(&bars.s_full[x]), t & 1, &s_abort, p.status, p.wait_cycles));
+            ok = wait(bars.s_full[x], t & 1);
             if (!ok) break;
             if constexpr (C::QUANT) {
-                ok = __all_sync(0xffffffffu, wait_or_abort(smem_u32(&bars.sc_full[n % kScaleSlots]), (n / kScaleSlots) & 1,
-                                                           &s_abort, p.status, p.wait_cycles));
+                ok = wait(bars.sc_full[n % kScaleSlots], (n / kScaleSlots) & 1);
                 if (!ok) break;
             }
             tc_fence_after();
+            // the row's 128 scores, kept in registers from here to P
+            float v[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, v[c]);
+            // per paged block of 16 keys (quantized pools): (K, V) scales, read where they are needed
             const float2* sc = s_scale + (C::QUANT ? (n % kScaleSlots) * kBlocks : 0);
             const int left = hi - lo - t * kBN;                   // keys of this tile in the range
             const bool need_mask = left < kBN;
-            // the row maximum of the tile's scaled scores, 64 at a time
-            float mx = -INFINITY;
+            tmem_wait_ld();
+            if (need_mask) {
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                float v[64];
-                tmem_ld32(tS + 64 * hh, *reinterpret_cast<float(*)[32]>(&v[0]));
-                tmem_ld32(tS + 64 * hh + 32, *reinterpret_cast<float(*)[32]>(&v[32]));
-                tmem_wait_ld();
-                if (need_mask) {
-#pragma unroll
-                    for (int j = 0; j < 64; ++j)
-                        if (64 * hh + j >= left) v[j] = -INFINITY;
-                }
-                float m4[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {                     // four paged blocks of 16 keys
-                    float m = fmaxf(v[16 * k], v[16 * k + 1]);
-#pragma unroll
-                    for (int j = 2; j < 16; j += 2) m = fmax3(m, v[16 * k + j], v[16 * k + j + 1]);
-                    // a scale of 0 would turn a masked -inf into NaN: its scores are 0
-                    if constexpr (C::QUANT) m = m == -INFINITY ? m : m * (sl * sc[4 * hh + k].x);
-                    m4[k] = m;
-                }
-                mx = fmax3(mx, fmax3(m4[0], m4[1], m4[2]), m4[3]);
+                for (int j = 0; j < kBN; ++j)
+                    if (j >= left) v[j >> 5][j & 31] = -INFINITY;
             }
+            // the row maximum of the scaled scores, in three-input maxima per paged block
+            float m8[kBlocks];
+#pragma unroll
+            for (int b8 = 0; b8 < kBlocks; ++b8) {
+                const float* w = &v[b8 >> 1][16 * (b8 & 1)];
+                float m0 = fmax3(w[0], w[1], w[2]), m1 = fmax3(w[3], w[4], w[5]);
+                m0 = fmax3(m0, w[6], w[7]);
+                m1 = fmax3(m1, w[8], w[9]);
+                m0 = fmax3(m0, w[10], w[11]);
+                m1 = fmax3(m1, w[12], w[13]);
+                m8[b8] = fmax3(m0, w[14], w[15]);
+                m8[b8] = fmaxf(m8[b8], m1);
+                // a block of scale 0 must not turn a masked -inf into NaN: its scores are 0
+                if constexpr (C::QUANT) m8[b8] = m8[b8] == -INFINITY ? m8[b8] : m8[b8] * (sl * sc[b8].x);
+            }
+            float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
             if constexpr (!C::QUANT) mx = mx == -INFINITY ? mx : mx * sl;
             float m_new = m_used;
             if (mx > m_used + kSlack || m_used == -INFINITY) m_new = mx;
@@ -499,48 +447,50 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                     tmem_st32(tO + 32 * c, o);
                 }
             }
-            // keys past the range: zero their V rows (P is 0 there, V may be stale or NaN).  Tiles
-            // that share V: A's warps, whose P.V runs first.  Converted tiles come zeroed.
-            if (!C::QUANT && need_mask && (!shared || x == 0)) {
+            // keys past the range: zero their V rows (P is 0 there, V may be stale or NaN).  Where A and
+            // B share V both do it, each before its own P.V.  Converted tiles come zeroed.
+            if (!C::QUANT && need_mask) {
                 const int s = n % NS;
-                ok = __all_sync(0xffffffffu, wait_or_abort(smem_u32(&bars.v_full[s]), (n / NS) & 1, &s_abort, p.status, p.wait_cycles));
+                ok = wait_tile(1, bars.v_full, n);
                 if (!ok) break;
-                const int tid = threadIdx.x - 64 - 128 * x;
+                const int tid = threadIdx.x & 127;
                 const int rows = kBN - left;
                 for (int i = tid; i < C::HALVES * rows * 8; i += 128) {
-                    const int c16 = i & 7, rowi = (i >> 3) % rows, half = (i >> 3) / rows;
-                    sts128(sV + s * TILE + half * (kBN * 128) + (left + rowi) * 128 + c16 * 16, 0u, 0u, 0u, 0u);
+                    const int c16 = i & 7, row = left + (i >> 3) % rows, half = (i >> 3) / rows;
+                    sts128(sV + s * TILE + (row >> 3) * KV<D>::GROUP + half * KV<D>::HALF + (row & 7) * 128 + c16 * 16, 0u,
+                           0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
+                __syncwarp();
             }
-            // P = 2^(sl S - m) in 16 bits, 32 keys at a time, packed into the tile's first 64 columns
-            // (the scores read from there are no longer needed)
+            // P = 2^(factor S - m) in 16 bits, packed into the tile's first 64 columns, in two halves
             const float2 mref2 = make_float2(-mref, -mref);
-            float2 sum2 = make_float2(0.f, 0.f);
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
+            float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            auto half_of_p = [&](int half, auto masked) {
 #pragma unroll
                 for (int cc = 0; cc < 2; ++cc) {
                     const int c = 2 * half + cc;
-                    float v[32];
-                    tmem_ld32(tS + 32 * c, v);
-                    tmem_wait_ld();
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        float s1 = sl, vm = 1.f;
+                        float f = sl;
+                        [[maybe_unused]] float vm = 1.f;
                         if constexpr (C::QUANT) {
                             const float2 kv = sc[2 * c + (e >> 3)];
-                            s1 = sl * kv.x;
+                            f = sl * kv.x;
                             vm = v_mul * kv.y;
                         }
-                        float2 a = ffma2(make_float2(v[2 * e], v[2 * e + 1]), make_float2(s1, s1), mref2);
-                        if (need_mask) {
+                        float2 a = ffma2(make_float2(v[c][2 * e], v[c][2 * e + 1]), make_float2(f, f), mref2);
+                        if constexpr (decltype(masked)::value) {   // again: -inf times a factor of 0 is NaN
                             if (32 * c + 2 * e >= left) a.x = -INFINITY;
                             if (32 * c + 2 * e + 1 >= left) a.y = -INFINITY;
                         }
-                        float2 pp = make_float2(ex2(a.x), ex2(a.y));
-                        sum2 = fadd2(sum2, pp);
+                        float2 pp;
+                        // some pairs take the FMA pipe, so that it shares the exponentials with
+                        // the special-function unit (not where -inf may stand)
+                        if (!decltype(masked)::value && e % kPolyEvery == kPolyEvery - 1) pp = exp2_poly<C::BF16 ? 3 : 4>(a);
+                        else pp = make_float2(ex2(a.x), ex2(a.y));
+                        sum2[e & 1] = fadd2(sum2[e & 1], pp);
                         if constexpr (C::QUANT) pp = fmul2(pp, make_float2(vm, vm));
                         w[e] = pack2<C::BF16>(pp.x, pp.y);
                     }
@@ -550,12 +500,19 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[x][half]));
+            };
+            if (need_mask) {
+                half_of_p(0, std::true_type{});
+                half_of_p(1, std::true_type{});
+            } else {
+                half_of_p(0, std::false_type{});
+                half_of_p(1, std::false_type{});
             }
-            l_run = l_run * alpha + (sum2.x + sum2.y);
+            l_run = l_run * alpha + ((sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y));
             m_used = m_new;
         }
         if (ok && nx > 0 &&
-            __all_sync(0xffffffffu, wait_or_abort(smem_u32(&bars.o_done[x]), 0, &s_abort, p.status, p.wait_cycles))) {
+            wait(bars.o_done[x], 0)) {
             tc_fence_after();
             const int rr = r0 + (PAIR ? 0 : x * kBM) + r;
             const bool valid = rr < R;
@@ -591,11 +548,136 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 __syncwarp();                                     // the next TMEM read needs the whole warp
             }
         }
+    } else if (warp < 12) {
+        regs_dec<72>();
+        if (warp == 8 || warp == 10) {
+        // ------------------------------------------------------------ producers (8: K, 10: V)
+        // The lanes hold the block ids of the next 4 key tiles of A and of B (one load per 4 tiles,
+        // a chunk ahead); one lane issues the copies, one box per paged block.  Keys past the range
+        // fetch block 0: in bounds, masked, and their V rows zeroed.
+        const bool is_v = warp == 10;
+        int cur[2], nxt[2];
+        auto entry = [&](int x, int i) -> int {
+            const int lb = key_lo(x) / kBlock + i;
+            return lb * kBlock < key_hi(x) ? block_id(lb) : 0;
+        };
+        for (int x = 0; x < 2; ++x) {
+            cur[x] = (x == 0 || nB > 0) ? entry(x, lane) : 0;
+            nxt[x] = (x == 0 || nB > 0) ? entry(x, 32 + lane) : 0;
+        }
+        constexpr int ND = C::QUANT ? NC : NS;                    // depth of the ring the copies go to
+        uint64_t* full = C::QUANT ? (is_v ? bars.cv_full : bars.ck_full) : (is_v ? bars.v_full : bars.k_full);
+        uint64_t* empty = C::QUANT ? (is_v ? bars.cv_empty : bars.ck_empty) : (is_v ? bars.v_empty : bars.k_empty);
+        constexpr uint32_t BYTES = C::QUANT ? C::CTILE : TILE;
+        constexpr uint32_t BOX = BYTES / kBlocks;                 // one paged block
+        const uint32_t ring = C::QUANT ? (is_v ? sCV : sCK) : (is_v ? sV : sK);
+        const CUtensorMap* tm = is_v ? &tmV : &tmK;
+        int issued = 0;
+        bool go = true;
+        const uint64_t pol = l2_evict_first();
+        const int tmax = max(nA, nB);
+        for (int t = 0; go && t < tmax; ++t) {
+            if (t > 0 && t % 4 == 0) {
+                for (int x = 0; x < 2; ++x) {
+                    cur[x] = nxt[x];
+                    if (x == 0 || nB > 0) nxt[x] = entry(x, (t / 4 + 1) * 32 + lane);
+                }
+            }
+            for (int x = 0; go && x < (shared ? 1 : 2); ++x) {
+                if (t >= (x == 0 ? nA : nB)) continue;
+                const int n = seq(x, t), s = n % ND;
+                int rows[kBlocks];
+#pragma unroll
+                for (int kb = 0; kb < kBlocks; ++kb)
+                    rows[kb] = (__shfl_sync(0xffffffffu, cur[x], (t % 4) * kBlocks + kb) * p.H_kv + g) * kBlock;
+                if (n >= ND) go = wait(empty[s], ((n - ND) / ND) & 1);
+                if (!go) break;
+                if (lane == 0) {
+                    const uint32_t bar = smem_u32(&full[s]), dst = ring + s * BYTES;
+                    mbar_arrive_expect_tx(bar, BYTES);
+                    if constexpr (!C::QUANT) s_armed[is_v ? 1 : 0] = n + 1;
+                    if (is_v || n != p.hold_tile) {   // test hook: the withheld tile's K bytes never arrive
+#pragma unroll
+                        for (int kb = 0; kb < kBlocks; ++kb) {
+                            if constexpr (C::QUANT) {
+                                if constexpr (PAIR) tma_load_2d_hint(dst + kb * BOX, tm, 0, rows[kb], bar, pol);
+                                else tma_load_2d(dst + kb * BOX, tm, 0, rows[kb], bar);
+                            } else {
+                                if constexpr (PAIR) tma_load_4d_hint(dst + kb * BOX, tm, 0, 0, 0, rows[kb] / 8, bar, pol);
+                                else tma_load_4d(dst + kb * BOX, tm, 0, 0, 0, rows[kb] / 8, bar);
+                            }
+                        }
+                    }
+                }
+                issued = n + 1;
+            }
+        }
+        // do not leave while copies into this CTA's shared memory may be in flight
+        if (lane == 0)
+            for (int n = max(0, issued - ND); n < issued; ++n)
+                if (is_v || n != p.hold_tile) mbar_wait_bounded(smem_u32(&full[n % ND]), (n / ND) & 1, p.wait_cycles);
+        } else {
+        // ------------------------------------------------------------ MMA issuers (9: tile A, 11: tile B)
+        // One warp per query tile, so that a wait of one tile's chain (P, the next K tile) does not
+        // keep the other tile's MMAs back.  The whole warp runs this loop; one elected lane issues
+        // each MMA and commit, all of a tile's from the same lane, so they run in order: S(t+1)
+        // overwrites the columns of P(t) after P.V(t) has read them.
+        const int x = warp == 9 ? 0 : 1;
+        const int nx = x == 0 ? nA : nB;
+        const uint32_t id_qk = idesc_f16(C::BF16, false, kBM, kBN);
+        const uint32_t id_pv = idesc_f16(C::BF16, true, kBM, D);
+        const uint32_t tS = tmem + 256 * x, tO = tS + 128;
+        const uint64_t dq = sdesc_k128(sQ + (PAIR ? 0 : x) * TILE);
+        const uint64_t dk = sdesc_k128_sbo(sK, KV<D>::GROUP), dv = sdesc_mn128_sbo(sV, KV<D>::HALF, KV<D>::GROUP);
+        bool ok = true;
+        auto scores = [&](int t) {              // S(x, t), and the release of its K tile
+            const int n = seq(x, t), s = n % NS;
+            ok = wait_tile(0, bars.k_full, n);
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t k0 = dk + (uint32_t)(s * (TILE >> 4));
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+                umma_w(tS, dq + (((ks >> 2) * (kBM * 128) + (ks & 3) * 32) >> 4),
+                       k0 + (((ks >> 2) * KV<D>::HALF + (ks & 3) * 32) >> 4), id_qk, ks > 0);
+            umma_commit_w(smem_u32(&bars.s_full[x]));
+            umma_commit_w(smem_u32(&bars.k_empty[s]));
+        };
+        if (nx > 0) scores(0);
+        for (int t = 0; ok && t < nx; ++t) {
+            const int n = seq(x, t), s = n % NS;
+            const uint64_t v0 = dv + (uint32_t)(s * (TILE >> 4));
+            ok = wait_tile(1, bars.v_full, n);
+#pragma unroll
+            for (int half = 0; ok && half < 2; ++half) {
+                ok = wait(bars.p_full[x][half], t & 1);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {   // 16 keys: two 8-row groups of V
+                    const int ks = 4 * half + k;
+                    umma_ts_w(tO, tS + 8 * ks, v0 + ((ks * 2 * KV<D>::GROUP) >> 4), id_pv, t > 0 || ks > 0);
+                }
+            }
+            if (!ok) break;
+            if (t + 1 < nx) {
+                umma_commit_w(smem_u32(&bars.v_empty[s]));
+                scores(t + 1);
+            } else {
+                umma_commit_w(smem_u32(&bars.o_done[x]));
+                umma_commit_w(smem_u32(&bars.v_empty[s]));
+            }
+        }
+        // every MMA that was issued, also on an abort, is done before TMEM is freed
+        umma_commit_w(smem_u32(&bars.mma_drain[x]));
+        mbar_wait_bounded(smem_u32(&bars.mma_drain[x]), 0, p.wait_cycles);
+        }
     } else if constexpr (C::QUANT) {
+        regs_dec<96>();
         // ------------------------------------------------------------ converters
         // One thread per key of a tile: its row of codes -> its row of the fp16 tile (both
         // swizzled by 16-byte chunks, so the 32 rows of a warp spread over the banks).
-        const int key = threadIdx.x - 320;                        // 0..127
+        const int key = threadIdx.x - 384;                        // 0..127
         auto convert = [&](uint32_t code, uint32_t dst, bool zero) {
             const int base = key * C::ROW;
             const int sw = (base >> 7) & C::SWZ;
@@ -610,7 +692,8 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                         uint32_t h[4];
                         codes8_int4(w[i], h);
                         const int ch = 4 * c + i;
-                        sts128(dst + (ch >> 3) * (kBN * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4), h[0], h[1], h[2], h[3]);
+                        sts128(dst + (key >> 3) * KV<D>::GROUP + (ch >> 3) * KV<D>::HALF + (key & 7) * 128 + (((ch & 7) ^ (key & 7)) << 4),
+                               h[0], h[1], h[2], h[3]);
                     }
                 } else {                                          // 16 elements: 2 chunks
 #pragma unroll
@@ -619,13 +702,11 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                         codes4<DT>(w[2 * i], h[0], h[1]);
                         codes4<DT>(w[2 * i + 1], h[2], h[3]);
                         const int ch = 2 * c + i;
-                        sts128(dst + (ch >> 3) * (kBN * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4), h[0], h[1], h[2], h[3]);
+                        sts128(dst + (key >> 3) * KV<D>::GROUP + (ch >> 3) * KV<D>::HALF + (key & 7) * 128 + (((ch & 7) ^ (key & 7)) << 4),
+                               h[0], h[1], h[2], h[3]);
                     }
                 }
             }
-        };
-        auto wait = [&](uint64_t& bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, wait_or_abort(smem_u32(&bar), parity, &s_abort, p.status, p.wait_cycles));
         };
         auto scales_of = [&](int x, int t) {                      // threads 0..7: one block of the tile each
             const int k = key_lo(x) + t * kBN + key * kBlock;
@@ -646,6 +727,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 const int left = key_hi(x) - key_lo(x) - t * kBN;
                 ok = wait(bars.ck_full[cs], (n / NC) & 1) && (n < NS || wait(bars.k_empty[s], ((n - NS) / NS) & 1));
                 if (!ok) break;
+                if (key == 0) s_armed[0] = n + 1;
                 if (key < kBlocks) s_scale[(n % kScaleSlots) * kBlocks + key] = mine;
                 convert(sCK + cs * C::CTILE, sK + s * TILE, false);
                 fence_proxy_async_smem();
@@ -657,6 +739,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 }
                 ok = wait(bars.cv_full[cs], (n / NC) & 1) && (n < NS || wait(bars.v_empty[s], ((n - NS) / NS) & 1));
                 if (!ok) break;
+                if (key == 0) s_armed[1] = n + 1;
                 convert(sCV + cs * C::CTILE, sV + s * TILE, key >= left);
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -671,7 +754,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) {
+    if (warp == 9) {
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
     }
 }

@@ -111,6 +111,22 @@ def test_groups_reports():
     assert pkv.read_device_status(pool) == pkv.DEV_BAD_LENGTH
 
 
+def test_groups_larger_than_their_bound_are_reported():
+    """Sequences past max_group_size are reported and left unwritten; the others are as they were."""
+    sizes, prefix, suffix = [3, 2], [64, 32], [5, 6, 7, 8, 9]
+    pool, opool, q, qd, tables, ctx = case(pkv.BF16, 128, 8, 2, sizes, prefix, suffix, 5850)
+    args = (tables.to(DEV), torch.tensor(ctx, dtype=torch.int32, device=DEV), starts_of(sizes).to(DEV),
+            torch.tensor(prefix, dtype=torch.int32, device=DEV), 0.1)
+    good = pkv.paged_decode_attn_groups(pool, 0, q.to(DEV), *args, 3, 64, 9)
+    out = torch.full(q.shape, 9.0, dtype=q.dtype, device=DEV)
+    pkv.paged_decode_attn_groups(pool, 0, q.to(DEV), *args, 2, 64, 9, out=out)
+    torch.cuda.synchronize()
+    assert pkv.read_device_status(pool) == pkv.DEV_BAD_LENGTH
+    assert (out[2] == 9).all()
+    keep = [0, 1, 3, 4]
+    assert torch.equal(out[keep], good[keep])
+
+
 def test_groups_captured_and_replayed():
     sizes, prefix, suffix = [6, 3], [512, 96], drawn(7, 9, 0, 150)
     pool, opool, q, qd, tables, ctx = case(pkv.FP8E4M3, 128, 16, 2, sizes, prefix, suffix, 5900)
