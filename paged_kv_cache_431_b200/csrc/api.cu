@@ -39,9 +39,12 @@ bool is_quantized(int dtype) { return dtype == PKV_INT8 || dtype == PKV_INT4 || 
 
 int num_sms()
 {
+    static std::atomic<int> known[64];   // by device; 0: not asked yet
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 148;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
@@ -673,9 +676,17 @@ struct RaggedSplit {
     int part, parts;
 };
 
-// Items of up to this many query rows per KV head run on the warp-level kernels, above on tcgen05.
-constexpr int kShortRows16 = 64;       // 16-bit pools: one K/V ring serves 64 rows
-constexpr int kShortRowsQuant = 16;    // quantized: each 16 rows read and convert the codes again
+// Items of up to this many query rows R per KV head run on the warp-level kernels, above on tcgen05
+// (whose time hardly depends on R up to 128).  Measured, head dim 128, warp-level against tcgen05:
+//   bf16, 64 sequences x 3,000 tokens x 8 KV heads: R 16 130 against 157 us, R 20 168 against 159;
+//   4 x 32,768: R 16 109 against 98, R 32 125 against 101, R 48 174 against 103;
+//   int8, the same: R 16 79-138 against 255, R 20 194 against 260, R 48 282 against 272;
+//   86 against 166, 151 against 168, 204 against 170.
+constexpr int kShortRows16 = 16;
+constexpr int kShortRowsQuant = 32;
+// One-warp CTAs per SM that a small batch is split into: 6 against 24 took int8, R 8, 4 x 32,768 from 97
+// to 67 us and an 8-sequence step from 38 to 27.
+constexpr int kRaggedCtas = 6;
 
 static RaggedSplit ragged_split(pkv_pool_t pool, int items, int max_rows, int G, int max_tokens)
 {
@@ -686,7 +697,14 @@ static RaggedSplit ragged_split(pkv_pool_t pool, int items, int max_rows, int G,
     r.tc = R > (quant ? kShortRowsQuant : kShortRows16);
     r.pair = r.tc && R <= 128;
     if (!r.tc) {
-        r.part = choose_partition(items, H_kv * (int)((R + 15) / 16), max_tokens, pool->row_bytes, quant, nullptr);
+        // ~256 (192) KiB of K + V per partition as in the plain decode, halved, down to 128 (192)
+        // tokens, only until every SM has kRaggedCtas one-warp CTAs: a partition's partials weigh R
+        // query rows, not G, so few long sequences are not cut as finely as there
+        int P = (quant ? 192 : 256) * 1024 / (2 * pool->row_bytes);
+        P = P < 128 ? 128 : (P > 4096 ? 4096 : P);
+        const long long ctas = (long long)items * H_kv * ((R + 15) / 16);
+        while (P >= 256 && ctas * ((max_tokens + P - 1) / P) < (long long)kRaggedCtas * num_sms()) P /= 2;
+        r.part = P;
     } else {
         // one CTA per SM: split the keys until two waves are full, in whole 128-key tiles, at
         // least two of them per partition

@@ -281,8 +281,10 @@ decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
             for (int nt = 0; nt < 2; ++nt) {
                 const float p0 = pr[nt][2 * hn], p1 = pr[nt][2 * hn + 1];
                 bh[hn][nt] = pack2<BF16>(p0, p1);
-                const float2 back = unpack2<BF16>(bh[hn][nt]);
-                bl[hn][nt] = pack2<BF16>(p0 - back.x, p1 - back.y);
+                if constexpr (!RAG) {   // the ragged output is 16-bit: one part of P is as exact as it is
+                    const float2 back = unpack2<BF16>(bh[hn][nt]);
+                    bl[hn][nt] = pack2<BF16>(p0 - back.x, p1 - back.y);
+                }
             }
 
         uint32_t keep01 = 0xffffffffu, keep23 = 0xffffffffu;
@@ -302,7 +304,7 @@ decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
 #pragma unroll
             for (int hn = 0; hn < NHT; ++hn) {
                 mma16816<BF16>(o[mt][hn], va, bh[hn][0], bh[hn][1]);
-                mma16816<BF16>(o[mt][hn], va, bl[hn][0], bl[hn][1]);
+                if constexpr (!RAG) mma16816<BF16>(o[mt][hn], va, bl[hn][0], bl[hn][1]);
             }
         }
 
@@ -372,10 +374,12 @@ decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
     const size_t row0 = (size_t)b * p.H_q + hbase;
     if constexpr (RAG) {
         // final rows rounded once to q's dtype; partials as in the plain form, by query row
-        for (int i = lane; i < GC * (D / 4); i += 32) {
-            const int h = i / (D / 4), c4 = i % (D / 4);
+        const int mine = lane < GC ? (int)ragged_row(it, p.G, p.H_q, g, 16 * hg + lane) : 0;
+        for (int i0 = 0; i0 < GC * (D / 4); i0 += 32) {
+            const int i = i0 + lane, h = i / (D / 4), c4 = i % (D / 4);
+            const size_t row = __shfl_sync(0xffffffffu, mine, h & 15);
+            if (h >= GC) break;
             const float4 v = *reinterpret_cast<const float4*>(&so[h * SR + 4 * c4]);
-            const size_t row = ragged_row(it, p.G, p.H_q, g, 16 * hg + h);
             if (final_out)
                 *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.rg.out16) + row * D + 4 * c4) = pack4(v, BF16);
             else

@@ -390,19 +390,29 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
     int eqr[2] = {0, 0};   // int8: the same per query row (rows r and r + 8)
     {
         const bool bf = p.q_bf16;
+        const uint16_t* qr[2];
         const uint16_t* qh = static_cast<const uint16_t*>(p.q) + ((size_t)b * p.H_q + hbase) * D;
-        auto qv = [&](int row, int dim) -> float {
-            uint16_t u;
-            if constexpr (RAG)
-                u = __ldg(static_cast<const uint16_t*>(p.q) +
-                          ragged_row(it, p.G, p.H_q, g, 16 * hg + row + dim / D) * D + dim % D);
-            else
-                u = __ldg(qh + row * D + dim);
+        if constexpr (RAG) {   // the lane's two query rows
+            qr[0] = static_cast<const uint16_t*>(p.q) + (r < GC ? ragged_row(it, p.G, p.H_q, g, 16 * hg + r) : 0) * D;
+            qr[1] = static_cast<const uint16_t*>(p.q) + (r + 8 < GC ? ragged_row(it, p.G, p.H_q, g, 16 * hg + r + 8) : 0) * D;
+        } else {
+            qr[0] = qh + r * D;
+            qr[1] = qh + (r + 8) * D;
+        }
+        auto as_float = [&](uint16_t u) -> float {
             return bf ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
         };
+        auto qv = [&](int hr, int dim) -> float { return as_float(__ldg(qr[hr] + dim)); };   // row r + 8 hr
         const bool r0 = r < GC, r1 = (NHT == 2) && (r + 8 < GC);
         float qmax = 0.f;
-        for (int i = lane; i < GC * D; i += 32) qmax = fmaxf(qmax, fabsf(qv(0, i)));
+        if constexpr (RAG) {
+            for (int i = 0; i < D / 4; ++i) {
+                if (r < GC) qmax = fmaxf(qmax, fabsf(qv(0, qd * (D / 4) + i)));
+                if (NHT == 2 && r + 8 < GC) qmax = fmaxf(qmax, fabsf(qv(1, qd * (D / 4) + i)));
+            }
+        } else {
+            for (int i = lane; i < GC * D; i += 32) qmax = fmaxf(qmax, fabsf(as_float(__ldg(qh + i))));
+        }
         eq = pow2_shift(warp_max(qmax));
         const float qs = pow2f(eq), qo = qs * ODD;
         if constexpr (KI8) {
@@ -412,11 +422,10 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
             for (int ks = 0; ks < KS8; ++ks)
 #pragma unroll
                 for (int reg = 0; reg < 4; ++reg) {
-                    const int row = r + 8 * (reg & 1);
                     const bool live = (reg & 1) ? (NHT == 2 && r + 8 < GC) : (r < GC);
 #pragma unroll
                     for (int jj = 0; jj < 4; ++jj)
-                        if (live) rm[reg & 1] = fmaxf(rm[reg & 1], fabsf(qv(row, qd * (D / 4) + 8 * ks + 4 * (reg >> 1) + jj)));
+                        if (live) rm[reg & 1] = fmaxf(rm[reg & 1], fabsf(qv(reg & 1, qd * (D / 4) + 8 * ks + 4 * (reg >> 1) + jj)));
                 }
 #pragma unroll
             for (int hr = 0; hr < 2; ++hr) {
@@ -428,12 +437,11 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
             for (int ks = 0; ks < KS8; ++ks)
 #pragma unroll
                 for (int reg = 0; reg < 4; ++reg) {   // a0: row r, dims +0; a1: r+8, +0; a2: r, +4; a3: r+8, +4
-                    const int row = r + 8 * (reg & 1);
                     const bool live = (reg & 1) ? (NHT == 2 && r + 8 < GC) : (r < GC);
                     uint32_t w0 = 0u, w1 = 0u;
 #pragma unroll
                     for (int jj = 0; jj < 4; ++jj) {
-                        const int Q = live ? __float2int_rn(qv(row, qd * (D / 4) + 8 * ks + 4 * (reg >> 1) + jj) *
+                        const int Q = live ? __float2int_rn(qv(reg & 1, qd * (D / 4) + 8 * ks + 4 * (reg >> 1) + jj) *
                                                             pow2f(eqr[reg & 1]))
                                            : 0;
                         const int d1 = (Q + 128) >> 8;
@@ -448,10 +456,10 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
         for (int ks = 0; ks < (KI8 ? 0 : Cfg::KS); ++ks) {
             const int d0 = kdim<DT, D>(ks, qd, 0), d1 = kdim<DT, D>(ks, qd, 1);
             const int d2 = kdim<DT, D>(ks, qd, 2), d3 = kdim<DT, D>(ks, qd, 3);
-            qa[ks][0] = r0 ? pack2<false>(qv(r, d0) * qs, qv(r, d1) * qs) : 0u;
-            qa[ks][2] = r0 ? pack2<false>(qv(r, d2) * qo, qv(r, d3) * qo) : 0u;
-            qa[ks][1] = r1 ? pack2<false>(qv(r + 8, d0) * qs, qv(r + 8, d1) * qs) : 0u;
-            qa[ks][3] = r1 ? pack2<false>(qv(r + 8, d2) * qo, qv(r + 8, d3) * qo) : 0u;
+            qa[ks][0] = r0 ? pack2<false>(qv(0, d0) * qs, qv(0, d1) * qs) : 0u;
+            qa[ks][2] = r0 ? pack2<false>(qv(0, d2) * qo, qv(0, d3) * qo) : 0u;
+            qa[ks][1] = r1 ? pack2<false>(qv(1, d0) * qs, qv(1, d1) * qs) : 0u;
+            qa[ks][3] = r1 ? pack2<false>(qv(1, d2) * qo, qv(1, d3) * qo) : 0u;
         }
         if constexpr (SUBN) {
 #pragma unroll
@@ -592,8 +600,10 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
             for (int nt = 0; nt < 2; ++nt) {
                 const float p0 = pr[nt][2 * hn] * sc_kv.y, p1 = pr[nt][2 * hn + 1] * sc_kv.y;
                 bh[hn][nt] = pack2<false>(p0, p1);
-                const float2 back = unpack2<false>(bh[hn][nt]);
-                bl[hn][nt] = pack2<false>(p0 - back.x, p1 - back.y);
+                if constexpr (!RAG) {   // the ragged output is 16-bit: one part of P is as exact as it is
+                    const float2 back = unpack2<false>(bh[hn][nt]);
+                    bl[hn][nt] = pack2<false>(p0 - back.x, p1 - back.y);
+                }
             }
 
         uint32_t keep01 = 0xffffffffu, keep23 = 0xffffffffu;
@@ -625,7 +635,7 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
 #pragma unroll
                 for (int hn = 0; hn < NHT; ++hn) {
                     mma16816<false>(o[mt][hn], va[jj], bh[hn][0], bh[hn][1]);
-                    mma16816<false>(o[mt][hn], va[jj], bl[hn][0], bl[hn][1]);
+                    if constexpr (!RAG) mma16816<false>(o[mt][hn], va[jj], bl[hn][0], bl[hn][1]);
                 }
             }
         }
@@ -676,10 +686,12 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
     }
     __syncwarp();
     if constexpr (RAG) {   // final rows rounded once to q's dtype; partials by query row
-        for (int i = lane; i < GC * (D / 4); i += 32) {
-            const int h = i / (D / 4), c4 = i % (D / 4);
+        const int mine = lane < GC ? (int)ragged_row(it, p.G, p.H_q, g, 16 * hg + lane) : 0;
+        for (int i0 = 0; i0 < GC * (D / 4); i0 += 32) {
+            const int i = i0 + lane, h = i / (D / 4), c4 = i % (D / 4);
+            const size_t row = __shfl_sync(0xffffffffu, mine, h & 15);
+            if (h >= GC) break;
             const float4 v = *reinterpret_cast<const float4*>(&so[h * SR + 4 * c4]);
-            const size_t row = ragged_row(it, p.G, p.H_q, g, 16 * hg + h);
             if (final_out)
                 *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.rg.out16) + row * D + 4 * c4) = pack4(v, p.q_bf16);
             else

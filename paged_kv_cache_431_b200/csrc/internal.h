@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <mutex>
 #include <vector>
 
@@ -47,6 +48,20 @@ int layer_maps(pkv_pool* pool, int layer, const CUtensorMap** tmk, const CUtenso
 int layer_block_maps(pkv_pool* pool, int layer, const CUtensorMap** tmk, const CUtensorMap** tmv);
 
 int num_sms();
+
+// cudaFuncSetAttribute(kernel, MaxDynamicSharedMemorySize, bytes), once per device and kernel (`done`:
+// a static of the launcher, one bit per device).
+template <typename K>
+inline bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
 
 struct DecodeArgs {
     const void* q;

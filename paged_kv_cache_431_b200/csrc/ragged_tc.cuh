@@ -43,10 +43,7 @@ constexpr int kBN = 128;                         // keys per tile
 constexpr int kBlocks = kBN / kBlock;            // paged blocks per key tile
 constexpr float kSlack = 8.f;                    // log2 units the running max may lag
 constexpr uint32_t kTmemCols = 512;              // tile x: S and P at 256x, O at 256x + 128
-#ifndef PKV_POLY_EVERY
-#define PKV_POLY_EVERY 4
-#endif
-constexpr int kPolyEvery = PKV_POLY_EVERY;       // of so many pairs of exponentials, one is a polynomial
+constexpr int kPolyEvery = 4;                    // of so many pairs of exponentials, one is a polynomial
 constexpr int kScaleSlots = 4;                   // key tiles whose scales are kept
 
 template <int D, int DT, bool PAIR>
@@ -83,7 +80,7 @@ struct KV {
 struct Bars {
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];    // 16-bit tiles, ready for the MMAs
     uint64_t ck_full[2], ck_empty[2], cv_full[2], cv_empty[2];   // code tiles
-    uint64_t sc_full[kScaleSlots];
+    uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];        // the scales of a key tile
     uint64_t s_full[2];        // S(x, t) is in TMEM, and every earlier MMA of the CTA is done
     uint64_t p_full[2][2];     // a half of P(x, t) is stored
     uint64_t o_done[2];
@@ -247,19 +244,22 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
         s_vmax = 0;
         s_armed[0] = s_armed[1] = 0;
         for (int s = 0; s < NS; ++s) {
-            mbar_init(smem_u32(&bars.k_full[s]), C::QUANT ? 4 : 1);
+            mbar_init(smem_u32(&bars.k_full[s]), C::QUANT ? 2 : 1);
             mbar_init(smem_u32(&bars.k_empty[s]), shared ? 2 : 1);
-            mbar_init(smem_u32(&bars.v_full[s]), C::QUANT ? 4 : 1);
+            mbar_init(smem_u32(&bars.v_full[s]), C::QUANT ? 2 : 1);
             mbar_init(smem_u32(&bars.v_empty[s]), shared ? 2 : 1);
         }
         if constexpr (C::QUANT) {
             for (int s = 0; s < NC; ++s) {
                 mbar_init(smem_u32(&bars.ck_full[s]), 1);
-                mbar_init(smem_u32(&bars.ck_empty[s]), 4);
+                mbar_init(smem_u32(&bars.ck_empty[s]), 2);
                 mbar_init(smem_u32(&bars.cv_full[s]), 1);
-                mbar_init(smem_u32(&bars.cv_empty[s]), 4);
+                mbar_init(smem_u32(&bars.cv_empty[s]), 2);
             }
-            for (int s = 0; s < kScaleSlots; ++s) mbar_init(smem_u32(&bars.sc_full[s]), 4);
+            for (int s = 0; s < kScaleSlots; ++s) {
+                mbar_init(smem_u32(&bars.sc_full[s]), 2);
+                mbar_init(smem_u32(&bars.sc_empty[s]), shared ? 8 : 4);
+            }
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(smem_u32(&bars.s_full[x]), 1);
@@ -287,7 +287,11 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
         }
         return blk;
     };
-    __syncthreads();                            // s_vmax and the barriers are initialised
+    // index of each query row, in rows of D (-1: none), where the first K tile will be
+    int* s_row = reinterpret_cast<int*>(smem + C::QT * TILE);
+    for (int i = threadIdx.x; i < C::QT * kBM; i += C::THREADS)
+        s_row[i] = r0 + i < R ? (int)ragged_row(it, p.G, p.H_q, g, r0 + i) : -1;
+    __syncthreads();                            // s_row, s_vmax and the barriers are initialised
 
     // ---- Q into shared memory, K-major with the 128-byte swizzle, by plain loads: rows are
     // gathered (row of the item, head), so any group size packs 128 rows into a tile.  A negative
@@ -298,9 +302,9 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
         const uint16_t* qh = static_cast<const uint16_t*>(p.q);
         for (int i = threadIdx.x; i < ((C::QT * kBM * CH + C::THREADS - 1) / C::THREADS) * C::THREADS; i += C::THREADS) {
             const int row = i / CH, c = i % CH;
-            const bool in = row < C::QT * kBM && r0 + row < R;
+            const int at = row < C::QT * kBM ? s_row[row] : -1;
             uint4 u = make_uint4(0u, 0u, 0u, 0u);
-            if (in) u = __ldg(reinterpret_cast<const uint4*>(qh + ragged_row(it, p.G, p.H_q, g, r0 + row) * D + 8 * c));
+            if (at >= 0) u = __ldg(reinterpret_cast<const uint4*>(qh + (size_t)at * D + 8 * c));
             uint32_t* w = reinterpret_cast<uint32_t*>(&u);
             if constexpr (C::QUANT) {           // fp16, times a power of two per row (its CH lanes agree on it)
                 float f[8], top = 0.f;
@@ -463,6 +467,14 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 fence_proxy_async_smem();
                 __syncwarp();
             }
+            // A and B take turns with the exponentials: left alone they fall into step, and then wait
+            // for the tensor cores together (617 -> 500 us on 1,024 rows x 8 heads against 4 x 4,096
+            // keys).  Quantized pools are bound by the conversions and run faster without it.
+            if (!C::QUANT && shared) {
+                if (x == 1) ok = wait(bars.p_full[0][1], t & 1);
+                else if (t > 0) ok = wait(bars.p_full[1][1], (t - 1) & 1);
+                if (!ok) break;
+            }
             // P = 2^(factor S - m) in 16 bits, packed into the tile's first 64 columns, in two halves
             const float2 mref2 = make_float2(-mref, -mref);
             float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -488,7 +500,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                         float2 pp;
                         // some pairs take the FMA pipe, so that it shares the exponentials with
                         // the special-function unit (not where -inf may stand)
-                        if (!decltype(masked)::value && e % kPolyEvery == kPolyEvery - 1) pp = exp2_poly<C::BF16 ? 3 : 4>(a);
+                        if (!C::QUANT && !decltype(masked)::value && e % kPolyEvery == kPolyEvery - 1) pp = exp2_poly<C::BF16 ? 3 : 4>(a);
                         else pp = make_float2(ex2(a.x), ex2(a.y));
                         sum2[e & 1] = fadd2(sum2[e & 1], pp);
                         if constexpr (C::QUANT) pp = fmul2(pp, make_float2(vm, vm));
@@ -507,6 +519,9 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
             } else {
                 half_of_p(0, std::false_type{});
                 half_of_p(1, std::false_type{});
+            }
+            if constexpr (C::QUANT) {
+                if (lane == 0) mbar_arrive(smem_u32(&bars.sc_empty[n % kScaleSlots]));
             }
             l_run = l_run * alpha + ((sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y));
             m_used = m_new;
@@ -675,12 +690,15 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
     } else if constexpr (C::QUANT) {
         regs_dec<96>();
         // ------------------------------------------------------------ converters
-        // One thread per key of a tile: its row of codes -> its row of the fp16 tile (both
-        // swizzled by 16-byte chunks, so the 32 rows of a warp spread over the banks).
-        const int key = threadIdx.x - 384;                        // 0..127
-        auto convert = [&](uint32_t code, uint32_t dst, bool zero) {
+        // Warps 12 and 13 convert K tiles, 14 and 15 V tiles, each at the pace of its ring.  A thread
+        // takes two keys of a tile: a row of codes -> a row of the fp16 tile (both swizzled by 16-byte
+        // chunks, so the 32 rows of a warp spread over the banks).
+        const bool is_v = warp >= 14;
+        const int id = threadIdx.x & 63;
+        auto convert = [&](uint32_t code, uint32_t dst, int key, bool zero) {
             const int base = key * C::ROW;
             const int sw = (base >> 7) & C::SWZ;
+            const uint32_t row = dst + (key >> 3) * KV<D>::GROUP + (key & 7) * 128;
 #pragma unroll
             for (int c = 0; c < C::ROW / 16; ++c) {
                 uint32_t w[4];
@@ -692,8 +710,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                         uint32_t h[4];
                         codes8_int4(w[i], h);
                         const int ch = 4 * c + i;
-                        sts128(dst + (key >> 3) * KV<D>::GROUP + (ch >> 3) * KV<D>::HALF + (key & 7) * 128 + (((ch & 7) ^ (key & 7)) << 4),
-                               h[0], h[1], h[2], h[3]);
+                        sts128(row + (ch >> 3) * KV<D>::HALF + (((ch & 7) ^ (key & 7)) << 4), h[0], h[1], h[2], h[3]);
                     }
                 } else {                                          // 16 elements: 2 chunks
 #pragma unroll
@@ -702,18 +719,22 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                         codes4<DT>(w[2 * i], h[0], h[1]);
                         codes4<DT>(w[2 * i + 1], h[2], h[3]);
                         const int ch = 2 * c + i;
-                        sts128(dst + (key >> 3) * KV<D>::GROUP + (ch >> 3) * KV<D>::HALF + (key & 7) * 128 + (((ch & 7) ^ (key & 7)) << 4),
-                               h[0], h[1], h[2], h[3]);
+                        sts128(row + (ch >> 3) * KV<D>::HALF + (((ch & 7) ^ (key & 7)) << 4), h[0], h[1], h[2], h[3]);
                     }
                 }
             }
         };
-        auto scales_of = [&](int x, int t) {                      // threads 0..7: one block of the tile each
-            const int k = key_lo(x) + t * kBN + key * kBlock;
-            if (key >= kBlocks || k >= key_hi(x)) return make_float2(0.f, 0.f);
+        auto scales_of = [&](int x, int t) {                      // K warps, threads 0..7: one block of the tile each
+            const int k = key_lo(x) + t * kBN + id * kBlock;
+            if (is_v || id >= kBlocks || k >= key_hi(x)) return make_float2(0.f, 0.f);
             const size_t i = (size_t)block_id(k / kBlock) * p.H_kv + g;
             return make_float2(p.k_scale[i], p.v_scale[i]);
         };
+        uint64_t* cfull = is_v ? bars.cv_full : bars.ck_full;
+        uint64_t* cempty = is_v ? bars.cv_empty : bars.ck_empty;
+        uint64_t* full = is_v ? bars.v_full : bars.k_full;
+        uint64_t* empty = is_v ? bars.v_empty : bars.k_empty;
+        const uint32_t from = is_v ? sCV : sCK, to = is_v ? sV : sK;
         bool ok = true;
         const int tmax = max(nA, nB);
         float2 next[2] = {scales_of(0, 0), nB > 0 ? scales_of(1, 0) : make_float2(0.f, 0.f)};
@@ -725,27 +746,21 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 const float2 mine = next[x];
                 if (t + 1 < nx) next[x] = scales_of(x, t + 1);
                 const int left = key_hi(x) - key_lo(x) - t * kBN;
-                ok = wait(bars.ck_full[cs], (n / NC) & 1) && (n < NS || wait(bars.k_empty[s], ((n - NS) / NS) & 1));
+                ok = wait(cfull[cs], (n / NC) & 1) && (n < NS || wait(empty[s], ((n - NS) / NS) & 1));
+                // the softmax warps release a slot of scales
+                if (!is_v && ok && n >= kScaleSlots) ok = wait(bars.sc_empty[n % kScaleSlots], ((n - kScaleSlots) / kScaleSlots) & 1);
                 if (!ok) break;
-                if (key == 0) s_armed[0] = n + 1;
-                if (key < kBlocks) s_scale[(n % kScaleSlots) * kBlocks + key] = mine;
-                convert(sCK + cs * C::CTILE, sK + s * TILE, false);
+                if (id == 0) s_armed[is_v ? 1 : 0] = n + 1;
+                if (!is_v && id < kBlocks) s_scale[(n % kScaleSlots) * kBlocks + id] = mine;
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k)
+                    convert(from + cs * C::CTILE, to + s * TILE, id + 64 * k, is_v && id + 64 * k >= left);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(smem_u32(&bars.sc_full[n % kScaleSlots]));
-                    mbar_arrive(smem_u32(&bars.k_full[s]));
-                    mbar_arrive(smem_u32(&bars.ck_empty[cs]));
-                }
-                ok = wait(bars.cv_full[cs], (n / NC) & 1) && (n < NS || wait(bars.v_empty[s], ((n - NS) / NS) & 1));
-                if (!ok) break;
-                if (key == 0) s_armed[1] = n + 1;
-                convert(sCV + cs * C::CTILE, sV + s * TILE, key >= left);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&bars.v_full[s]));
-                    mbar_arrive(smem_u32(&bars.cv_empty[cs]));
+                    if (!is_v) mbar_arrive(smem_u32(&bars.sc_full[n % kScaleSlots]));
+                    mbar_arrive(smem_u32(&full[s]));
+                    mbar_arrive(smem_u32(&cempty[cs]));
                 }
             }
         }
@@ -764,8 +779,8 @@ int launch(const DecodeParams& p, int items, int max_rows, const CUtensorMap* tm
 {
     using C = Cfg<D, DT, PAIR>;
     auto kern = ragged_tc_kernel<D, DT, PAIR>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-        return PKV_ERR_CUDA;
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(kern, C::SMEM, done)) return PKV_ERR_CUDA;
     const int zparts = PAIR ? (p.max_parts + 1) / 2 : p.max_parts;
     const dim3 grid((max_rows * p.G + C::QT * kBM - 1) / (C::QT * kBM), p.H_kv, items * zparts);
     kern<<<grid, C::THREADS, C::SMEM, s>>>(p, *tmk, *tmv);

@@ -271,64 +271,61 @@ def kv_append(pool: KVPool, layer: int, k: torch.Tensor, v: torch.Tensor, slot_m
                            else 0, _stream(stream)), "kv_append")
 
 
-class _OnDevice:
-    """What the calls below share: all tensors on one CUDA device, which is made current for the
-    launch if it is not; a workspace taken from torch's allocator stays reserved for the stream
-    that the call runs on."""
+# What the calls below share: all tensors on the pool's device, which is made current for the
+# launch if it is not; plain integers as pointers (ctypes converts them fastest); a workspace or
+# output taken from torch's allocator stays reserved for the stream that the call was given.
 
-    def __init__(self, device, stream, *tensors):
-        if device.type != "cuda":
-            raise ValueError("expected CUDA tensors")
-        for t in tensors:
-            if t is not None and t.device != device:
-                raise ValueError(f"tensors on {device} and {t.device}")
-        self.device = device
-        self.given = stream
-        self.before = None
-
-    def __enter__(self):
-        now = torch.cuda.current_device()
-        if self.device.index != now:
-            self.before = now
-            torch.cuda.set_device(self.device)
-        return self
-
-    def __exit__(self, *exc):
-        if self.before is not None:
-            torch.cuda.set_device(self.before)
-
-    def stream(self):
-        return _stream(self.given)
-
-    def empty(self, n: int):
-        ws = torch.empty(n, dtype=torch.uint8, device=self.device)
-        self.keep(ws)
-        return ws
-
-    def keep(self, t: torch.Tensor):
-        if self.given is not None:
-            s = self.given if hasattr(self.given, "cuda_stream") else torch.cuda.ExternalStream(int(self.given),
-                                                                                                 self.device)
-            t.record_stream(s)
+def _device_index(pool: KVPool, *tensors) -> int:
+    idx = pool.__dict__.get("_dev")
+    if idx is None:
+        t = pool.k_data[0] if isinstance(pool.k_data, list) else pool.k_data
+        idx = pool._dev = t.get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != idx:
+            raise ValueError("expected CUDA tensors on the pool's device")
+    return idx
 
 
-def _pool_device(pool: KVPool):
-    t = pool.k_data[0] if isinstance(pool.k_data, list) else pool.k_data
-    return t.device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _int32(t: torch.Tensor, n: int | None = None, what: str = "index tensor") -> ctypes.c_void_p:
-    if t.dtype != torch.int32 or not t.is_contiguous() or (n is not None and t.numel() != n):
-        raise ValueError(f"{what}: expected a contiguous int32 tensor" + ("" if n is None else f" of {n} elements"))
-    return ctypes.c_void_p(t.data_ptr())
+def _stream_of(stream, idx: int) -> int:
+    if stream is None:
+        return _raw_stream(idx) if _raw_stream is not None else torch.cuda.current_stream(idx).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _keep(t: torch.Tensor, stream, idx: int) -> torch.Tensor:
+    if stream is not None:
+        t.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), idx))
+    return t
+
+
+def _ws(workspace, need: int, stream, idx: int):
+    """(workspace tensor, address, bytes) of a caller's workspace, or of one taken here."""
+    if workspace is None:
+        if not need:
+            return None, 0, 0
+        workspace = _keep(torch.empty(need, dtype=torch.uint8, device=idx), stream, idx)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _int32(t: torch.Tensor, n: int, what: str) -> int:
+    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous int32 tensor of {n} elements")
+    return t.data_ptr()
 
 
 def _rows(t: torch.Tensor, T: int, heads: int, d: int, what: str):
-    """(pointer, elements per token) of [T, heads, d] rows that are dense within a token."""
-    if t.shape != (T, heads, d) or (T and heads and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d))):
-        raise ValueError(f"{what}: expected [{T}, {heads}, {d}] with dense rows")
-    # a single token may carry any stride; it is not used
-    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if T > 1 else heads * d)
+    """(address, elements per token) of [T, heads, d] rows that are dense within a token."""
+    if t.shape != (T, heads, d):
+        raise ValueError(f"{what}: expected [{T}, {heads}, {d}]")
+    s = t.stride()
+    if T and heads and (s[2] != 1 or (heads > 1 and s[1] != d)):
+        raise ValueError(f"{what}: expected rows that are dense within a token")
+    return t.data_ptr(), (s[0] if T > 1 else heads * d)   # one token may carry any stride
 
 
 def kv_append_rope_workspace_bytes(pool: KVPool, num_tokens: int) -> int:
@@ -346,35 +343,36 @@ def kv_append_rope(pool: KVPool, layer: int, q: torch.Tensor | None, k: torch.Te
     neighbouring dims instead of the halves.  q, k and v may be views of one projection's output
     (dense within a token).  q_out may be q.  Rows of padding (negative slots) are not written.
     q None appends only."""
+    idx = _device_index(pool, q, k, v, positions, cos_sin, slot_mapping, q_out, workspace)
+    if idx != torch.cuda.current_device():
+        with torch.cuda.device(idx):
+            return kv_append_rope(pool, layer, q, k, v, positions, cos_sin, slot_mapping, q_out, interleaved, workspace,
+                                  stream)
     T, d = slot_mapping.shape[0], pool.head_dim
-    dev = _pool_device(pool)
-    with _OnDevice(dev, stream, q, k, v, positions, cos_sin, slot_mapping, q_out, workspace) as on:
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-            raise ValueError("cos_sin: expected a contiguous fp32 [max_positions, rotary_dim] tensor")
-        H_q = 0 if q is None else q.shape[1]
-        kp, ks = _rows(k, T, pool.num_kv_heads, d, "k")
-        vp, vs = _rows(v, T, pool.num_kv_heads, d, "v")
-        qp = qop = None
-        qs = qos = 0
-        if k.dtype != v.dtype or (q is not None and q.dtype != k.dtype):
-            raise ValueError("q, k and v must have one dtype")
-        if q is not None:
-            qp, qs = _rows(q, T, H_q, d, "q")
-            if q_out is None:
-                q_out = torch.empty(T, H_q, d, dtype=q.dtype, device=dev)
-                on.keep(q_out)
-            if q_out.dtype != q.dtype:
-                raise ValueError("q_out must have q's dtype")
-            qop, qos = _rows(q_out, T, H_q, d, "q_out")
-        need = kv_append_rope_workspace_bytes(pool, T)
-        if need and workspace is None:
-            workspace = on.empty(need)
-        rope = _Rope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0)
-        _check(lib().kv_append_rope(pool.handle, layer, qp, qs, kp, ks, vp, vs, _dtype_code(k), ctypes.byref(rope),
-                                    _int32(positions, T, "positions"), _int32(slot_mapping, T, "slot_mapping"), T, H_q,
-                                    qop, qos, _ptr(workspace),
-                                    workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                                    on.stream()), "kv_append_rope")
+    if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin: expected a contiguous fp32 [max_positions, rotary_dim] tensor")
+    kp, ks = _rows(k, T, pool.num_kv_heads, d, "k")
+    vp, vs = _rows(v, T, pool.num_kv_heads, d, "v")
+    if k.dtype is not v.dtype:
+        raise ValueError("q, k and v must have one dtype")
+    qp = qs = qop = qos = H_q = 0
+    if q is not None:
+        if q.dim() != 3 or q.dtype is not k.dtype:
+            raise ValueError("q, k and v must be [T, heads, head_dim] of one dtype")
+        H_q = q.shape[1]
+        qp, qs = _rows(q, T, H_q, d, "q")
+        if q_out is None:
+            q_out = _keep(torch.empty(T, H_q, d, dtype=q.dtype, device=idx), stream, idx)
+        elif q_out.dtype is not q.dtype:
+            raise ValueError("q_out must have q's dtype")
+        qop, qos = _rows(q_out, T, H_q, d, "q_out")
+    need = kv_append_rope_workspace_bytes(pool, T) if pool.kv_dtype in QUANTIZED else 0
+    workspace, wp, wb = _ws(workspace, need, stream, idx)
+    shape = cos_sin.shape
+    rope = _Rope(cos_sin.data_ptr(), shape[0], shape[1], 1 if interleaved else 0)
+    _check(lib().kv_append_rope(pool.handle, layer, qp, qs, kp, ks, vp, vs, _dtype_code(k), ctypes.byref(rope),
+                                _int32(positions, T, "positions"), _int32(slot_mapping, T, "slot_mapping"), T, H_q,
+                                qop, qos, wp, wb, _stream_of(stream, idx)), "kv_append_rope")
     return q_out
 
 
@@ -441,32 +439,21 @@ def paged_decode_attn_cascade(pool: KVPool, layer: int, q: torch.Tensor, block_t
     return out
 
 
-def _ragged_out(on, q, out):
-    if not q.is_contiguous() or q.dim() != 3:
-        raise ValueError("q: expected a contiguous [rows, H_q, head_dim] tensor")
+def _ragged_rows(pool: KVPool, q, out, stream, idx: int):
+    if q.dim() != 3 or not q.is_contiguous() or q.shape[2] != pool.head_dim:
+        raise ValueError(f"q: expected a contiguous [rows, H_q, {pool.head_dim}] tensor")
     if out is None:
-        out = torch.empty_like(q)
-        on.keep(out)
-    if out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
+        return _keep(torch.empty_like(q), stream, idx)
+    if out.dtype is not q.dtype or out.shape != q.shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of q's shape and dtype")
     return out
 
 
 def _tables(t: torch.Tensor, n: int):
+    """(address, width) of block tables of n sequences."""
     if t.dim() != 2 or t.shape[0] != n:
         raise ValueError(f"block_tables: expected [{n}, width]")
-    return _int32(t, None, "block_tables")
-
-
-def _check_head_dim(pool: KVPool, q: torch.Tensor):
-    if q.shape[2] != pool.head_dim:
-        raise ValueError(f"q has head dim {q.shape[2]}, the pool {pool.head_dim}")
-
-
-def _ws(on, workspace, need: int):
-    if need and workspace is None:
-        workspace = on.empty(need)
-    return _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return _int32(t, t.numel(), "block_tables"), t.shape[1]
 
 
 def paged_cross_workspace_bytes(pool: KVPool, total_rows: int, num_q_heads: int, num_seqs: int, max_rows: int,
@@ -482,18 +469,21 @@ def paged_cross_attn(pool: KVPool, layer: int, q: torch.Tensor, row_starts: torc
     """Attention of a ragged batch of rows q [rows, H_q, head_dim] to all cached tokens of their
     sequences: rows row_starts[b] .. row_starts[b+1]-1 belong to sequence b (int32 [B + 1]).
     Returns out in q's dtype; rows of no sequence are left as they are."""
-    dev = _pool_device(pool)
-    with _OnDevice(dev, stream, q, row_starts, block_tables, context_lens, out, workspace) as on:
-        out = _ragged_out(on, q, out)
-        _check_head_dim(pool, q)
-        rows, H_q, _ = q.shape
-        B = context_lens.shape[0]
-        wp, wb = _ws(on, workspace, paged_cross_workspace_bytes(pool, rows, H_q, B, max_rows, max_context_len))
-        _check(lib().paged_cross_attn(pool.handle, layer, _ptr(q), _dtype_code(q),
-                                      _int32(row_starts, B + 1, "row_starts"), rows, H_q, _tables(block_tables, B),
-                                      block_tables.shape[1], _int32(context_lens, B, "context_lens"), B, max_rows,
-                                      max_context_len, float(scale), _ptr(out), wp, wb, on.stream()),
-               "paged_cross_attn")
+    idx = _device_index(pool, q, row_starts, block_tables, context_lens, out, workspace)
+    if idx != torch.cuda.current_device():
+        with torch.cuda.device(idx):
+            return paged_cross_attn(pool, layer, q, row_starts, block_tables, context_lens, scale, max_rows,
+                                    max_context_len, out, workspace, stream)
+    out = _ragged_rows(pool, q, out, stream, idx)
+    rows, H_q, _ = q.shape
+    B = context_lens.shape[0]
+    need = 0 if workspace is not None else paged_cross_workspace_bytes(pool, rows, H_q, B, max_rows, max_context_len)
+    workspace, wp, wb = _ws(workspace, need, stream, idx)
+    tp, width = _tables(block_tables, B)
+    _check(lib().paged_cross_attn(pool.handle, layer, q.data_ptr(), _dtype_code(q), _int32(row_starts, B + 1, "row_starts"),
+                                  rows, H_q, tp, width, _int32(context_lens, B, "context_lens"), B, max_rows,
+                                  max_context_len, scale, out.data_ptr(), wp, wb, _stream_of(stream, idx)),
+           "paged_cross_attn")
     return out
 
 
@@ -511,20 +501,23 @@ def paged_decode_attn_groups(pool: KVPool, layer: int, q: torch.Tensor, block_ta
     """Decode attention for a batch in groups: sequences group_starts[g] .. group_starts[g+1]-1
     (int32 [groups + 1]) share their first prefix_lens[g] tokens, a multiple of 16.  Returns out
     [B, H_q, head_dim] in q's dtype; rows of sequences in no group are left as they are."""
-    dev = _pool_device(pool)
-    with _OnDevice(dev, stream, q, block_tables, context_lens, group_starts, prefix_lens, out, workspace) as on:
-        out = _ragged_out(on, q, out)
-        _check_head_dim(pool, q)
-        B, H_q, _ = q.shape
-        n = prefix_lens.shape[0]
-        wp, wb = _ws(on, workspace, paged_decode_groups_workspace_bytes(pool, B, H_q, n, max_group_size,
-                                                                        max_prefix_len, max_suffix_len))
-        _check(lib().paged_decode_attn_groups(pool.handle, layer, _ptr(q), _dtype_code(q), _tables(block_tables, B),
-                                              block_tables.shape[1], _int32(context_lens, B, "context_lens"), B, H_q,
-                                              _int32(group_starts, n + 1, "group_starts"),
-                                              _int32(prefix_lens, n, "prefix_lens"), n, max_group_size,
-                                              max_prefix_len, max_suffix_len, float(scale), _ptr(out), wp, wb,
-                                              on.stream()), "paged_decode_attn_groups")
+    idx = _device_index(pool, q, block_tables, context_lens, group_starts, prefix_lens, out, workspace)
+    if idx != torch.cuda.current_device():
+        with torch.cuda.device(idx):
+            return paged_decode_attn_groups(pool, layer, q, block_tables, context_lens, group_starts, prefix_lens, scale,
+                                            max_group_size, max_prefix_len, max_suffix_len, out, workspace, stream)
+    out = _ragged_rows(pool, q, out, stream, idx)
+    B, H_q, _ = q.shape
+    n = prefix_lens.shape[0]
+    need = 0 if workspace is not None else paged_decode_groups_workspace_bytes(pool, B, H_q, n, max_group_size,
+                                                                               max_prefix_len, max_suffix_len)
+    workspace, wp, wb = _ws(workspace, need, stream, idx)
+    tp, width = _tables(block_tables, B)
+    _check(lib().paged_decode_attn_groups(pool.handle, layer, q.data_ptr(), _dtype_code(q), tp, width,
+                                          _int32(context_lens, B, "context_lens"), B, H_q,
+                                          _int32(group_starts, n + 1, "group_starts"), _int32(prefix_lens, n, "prefix_lens"),
+                                          n, max_group_size, max_prefix_len, max_suffix_len, scale, out.data_ptr(), wp,
+                                          wb, _stream_of(stream, idx)), "paged_decode_attn_groups")
     return out
 
 
