@@ -194,7 +194,7 @@ PKV_API size_t kv_append_rope_workspace_bytes(pkv_pool_t pool, int num_tokens);
  *        else it must not overlap an input.
  *   positions [device]: int32 [num_tokens], in [0, rope->max_positions).
  *   slot_mapping [device]: int32 [num_tokens].  A token with a negative slot is padding: nothing
- *        is read or written for it, its q_out row included.  Two tokens of one call must not
+ *        is written for it, its q_out row included.  Two tokens of one call must not
  *        share a slot.
  *   workspace [device]: kv_append_rope_workspace_bytes(pool, num_tokens) bytes.
  * A token whose slot or position is out of range is skipped like padding and sets

@@ -849,7 +849,7 @@ int paged_decode_attn_groups(pkv_pool_t pool, int layer, const void* q, int q_dt
     if (rc != PKV_OK) return rc;
     if (max_prefix_len < 0 || max_suffix_len < 0 || (long long)max_prefix_len + max_suffix_len > 0x7fffffffLL)
         return PKV_ERR_ARG;
-    if (num_seqs > 65535) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs > 65534) return PKV_ERR_UNSUPPORTED;   // grid z: the sequences and one more
     if (num_seqs == 0 || num_groups == 0 || max_group_size == 0) return PKV_OK;
     if (!block_tables || !context_lens || !group_starts || !prefix_lens) return PKV_ERR_NULL;
     RaggedArgs a = ragged_args(pool, layer, q, q_dtype, num_q_heads, scale, num_seqs, block_tables, block_table_width,
@@ -887,6 +887,7 @@ int paged_decode_attn_groups(pkv_pool_t pool, int layer, const void* q, int q_dt
     a.max_parts = own.parts;
     a.part_base = pre.parts;
     a.pre_part = pre.part;
+    a.beside = pre.parts > 0 && !own.tc;
     rc = launch_ragged(pool, layer, a, own, s);
     if (rc != PKV_OK || slots <= 1) return rc;
     return launch_ragged_merge(a, s);

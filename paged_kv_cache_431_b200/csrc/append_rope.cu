@@ -42,6 +42,7 @@ constexpr int kRopeThreads = 256;
 // Up to this many tokens every CTA scans the slots (two loads per thread); above it the scan
 // would cost more than the extra launch.
 constexpr int kScanTokens = 512;
+constexpr int kLook = 4;   // tokens per CTA where the tokens of a block are looked up
 
 struct RopeParams {
     const uint16_t* q;
@@ -117,15 +118,36 @@ __device__ __forceinline__ void copy_rows(const RopeParams& p, int cta)
 {
     constexpr int UNITS = D / 16;                       // units per row
     constexpr int STEP = kRopeThreads / UNITS;          // rows in flight per CTA
+    constexpr int BATCH = 3;                            // rows of a thread in flight together
     const int t = cta / p.copy_y, y = cta % p.copy_y;
     const int u = threadIdx.x % UNITS;
-    const int slot = p.slots[t], pos = p.positions[t];
-    if (!live(p, slot, pos, threadIdx.x == 0 && y == 0)) return;
     const int half = p.rot / 2;
     const bool rotated = 16 * u < p.rot;
     // the unit's two chunks, and the first of its 8 angles
     const int d0 = rotated && !p.inter ? 8 * u : 16 * u;
     const int d1 = rotated && !p.inter ? half + 8 * u : 16 * u + 8;
+    const int slot = p.slots[t], pos = p.positions[t];
+    const int step = p.copy_y * STEP;
+    uint4 x[BATCH][2];
+    auto source = [&](int row) -> const uint16_t* {
+        if (row < p.H_q) return p.q + t * p.q_stride + row * D;
+        const int h = row - p.H_q;
+        return h < p.H_kv ? p.k + t * p.k_stride + h * D : p.v + t * p.v_stride + (h - p.H_kv) * D;
+    };
+    auto load = [&](int row0) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int row = row0 + i * step;
+            if (row < p.rows) {
+                const uint16_t* src = source(row);
+                x[i][0] = *reinterpret_cast<const uint4*>(src + d0);
+                x[i][1] = *reinterpret_cast<const uint4*>(src + d1);
+            }
+        }
+    };
+    const int first = y * STEP + threadIdx.x / UNITS;
+    load(first);                                        // in flight with the slot and the position
+    if (!live(p, slot, pos, threadIdx.x == 0 && y == 0)) return;
     float c[8], s[8];
     if (rotated) {
         const float4* cs = reinterpret_cast<const float4*>(p.table + (size_t)pos * p.rot + 8 * u);
@@ -136,62 +158,83 @@ __device__ __forceinline__ void copy_rows(const RopeParams& p, int cta)
         *reinterpret_cast<float4*>(&s[4]) = __ldg(sn + 1);
     }
     const size_t blk = slot / kBlock, off = slot % kBlock;
-#pragma unroll 2
-    for (int row = y * STEP + threadIdx.x / UNITS; row < p.rows; row += p.copy_y * STEP) {
-        const uint16_t* src;
-        uint16_t* dst;
-        bool r = rotated;
-        if (row < p.H_q) {
-            src = p.q + t * p.q_stride + row * D;
-            dst = p.q_out + t * p.q_out_stride + row * D;
-        } else {
-            const bool is_v = row >= p.H_q + p.H_kv;
-            const int h = row - p.H_q - (is_v ? p.H_kv : 0);
-            src = is_v ? p.v + t * p.v_stride + h * D : p.k + t * p.k_stride + h * D;
-            dst = reinterpret_cast<uint16_t*>(is_v ? p.v_pool : p.k_pool) + ((blk * p.H_kv + h) * kBlock + off) * D;
-            r = rotated && !is_v;
+    for (int row0 = first; row0 < p.rows; row0 += BATCH * step) {
+        if (row0 != first) load(row0);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int row = row0 + i * step;
+            if (row >= p.rows) break;
+            const bool is_q = row < p.H_q, is_v = row >= p.H_q + p.H_kv;
+            uint16_t* dst;
+            if (is_q) {
+                dst = p.q_out + t * p.q_out_stride + row * D;
+            } else {
+                const int h = row - p.H_q - (is_v ? p.H_kv : 0);
+                dst = reinterpret_cast<uint16_t*>(is_v ? p.v_pool : p.k_pool) + ((blk * p.H_kv + h) * kBlock + off) * D;
+            }
+            if (rotated && !is_v) turn_unit<BF16>(x[i][0], x[i][1], c, s, p.inter);
+            *reinterpret_cast<uint4*>(dst + d0) = x[i][0];
+            *reinterpret_cast<uint4*>(dst + d1) = x[i][1];
         }
-        uint4 x0 = *reinterpret_cast<const uint4*>(src + d0);
-        uint4 x1 = *reinterpret_cast<const uint4*>(src + d1);
-        if (r) turn_unit<BF16>(x0, x1, c, s, p.inter);
-        *reinterpret_cast<uint4*>(dst + d0) = x0;
-        *reinterpret_cast<uint4*>(dst + d1) = x1;
     }
 }
 
 // ---------------------------------------------------------------- quantized --
-// One CTA per token; it works only if the token is the first written one of its block.  Each
-// warp takes (head, K or V) tiles in turn: D/8 lanes hold one row (8 elements each, two runs of
-// 4), so 32 / (D/8) rows per pass and at most D/16 passes over the block's 16 rows.
+// A CTA looks at `kLook` tokens (one where the slots are scanned); of these it works on the ones that
+// are the first written token of their block, on K or on V.  Each warp takes (block, head) tiles in turn:
+// D/8 lanes hold one row (8 elements each, two runs of 4), so 32 / (D/8) rows per pass and at most
+// D/16 passes over the block's 16 rows; passes without a token are skipped.
 template <int D, bool BF16, int DT>
-__device__ __forceinline__ void quantize_block(const RopeParams& p, int t)
+__device__ __forceinline__ void quantize_block(const RopeParams& p, int cta, bool is_v)
 {
     constexpr int LPR = D / 8, RPP = 32 / LPR, PASSES = kBlock / RPP;
     constexpr int RB = DT == PKV_INT4 ? D / 2 : D;
-    __shared__ int tok_of[kBlock];
+    __shared__ int tok_of[kLook][kBlock], pos_of[kLook][kBlock], blk_of[kLook];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int slot = p.slots[t];
-    if (!live(p, slot, p.positions[t], threadIdx.x == 0)) return;
-    const int blk = slot / kBlock;
+    const int look = p.index ? kLook : 1;
     if (p.index) {
-        if (threadIdx.x < kBlock) {
-            const int s = blk * kBlock + threadIdx.x;
-            const int o = p.index[s];
-            tok_of[threadIdx.x] = ((unsigned)o < (unsigned)p.T && p.slots[o] == s && live(p, s, p.positions[o], false)) ? o : -1;
+        const int i = threadIdx.x / kBlock, o16 = threadIdx.x % kBlock;
+        if (i < kLook) {
+            const int t = cta * kLook + i;
+            const int slot = t < p.T ? p.slots[t] : -1;
+            const bool in = t < p.T && live(p, slot, p.positions[t], o16 == 0);
+            int tok = -1, pos = 0;
+            if (in) {
+                const int s = slot / kBlock * kBlock + o16;
+                const int o = p.index[s];
+                if ((unsigned)o < (unsigned)p.T && p.slots[o] == s) {
+                    pos = p.positions[o];
+                    if (live(p, s, pos, false)) tok = o;
+                }
+            }
+            // the block's first written token: the lowest offset that has one
+            const unsigned have = (__ballot_sync(0xffffffffu, tok >= 0) >> (threadIdx.x & 16)) & 0xffffu;
+            const int lead = __shfl_sync(0xffffffffu, tok, (threadIdx.x & 16) + (have ? __ffs(have) - 1 : 0));
+            tok_of[i][o16] = tok;
+            pos_of[i][o16] = pos;
+            if (o16 == 0) blk_of[i] = in && lead == t ? slot / kBlock : -1;
         }
         __syncthreads();
     } else {
-        if (threadIdx.x < kBlock) tok_of[threadIdx.x] = -1;
+        const int t = cta;
+        const int slot = p.slots[t];
+        if (!live(p, slot, p.positions[t], threadIdx.x == 0)) return;
+        if (threadIdx.x < kBlock) tok_of[0][threadIdx.x] = -1;
         __syncthreads();
         for (int o = threadIdx.x; o < p.T; o += kRopeThreads) {
             const int s = p.slots[o];
-            if (s >= 0 && s / kBlock == blk && live(p, s, p.positions[o], false)) atomicMax(&tok_of[s % kBlock], o);
+            if (s >= 0 && s / kBlock == slot / kBlock && live(p, s, p.positions[o], false)) atomicMax(&tok_of[0][s % kBlock], o);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            const int tok = lane < kBlock ? tok_of[0][lane] : -1;
+            const unsigned have = __ballot_sync(0xffffffffu, tok >= 0);
+            const int lead = __shfl_sync(0xffffffffu, tok, have ? __ffs(have) - 1 : 0);
+            if (lane < kBlock) pos_of[0][lane] = tok >= 0 ? p.positions[tok] : 0;
+            if (lane == 0) blk_of[0] = lead == t ? slot / kBlock : -1;
         }
         __syncthreads();
     }
-    int first = 0;
-    while (first < kBlock && tok_of[first] < 0) ++first;
-    if (first == kBlock || tok_of[first] != t) return;   // another token leads this block
 
     const int half = p.rot / 2;
     const int sub = lane / LPR, ln = lane % LPR;
@@ -200,17 +243,24 @@ __device__ __forceinline__ void quantize_block(const RopeParams& p, int t)
     const bool rotated = 8 * ln < p.rot;
     const int d0 = rotated && !p.inter ? 4 * ln : 8 * ln;
     const int d1 = rotated && !p.inter ? half + 4 * ln : 8 * ln + 4;
-    for (int task = warp; task < 2 * p.H_kv; task += kRopeThreads / 32) {
-        const bool is_v = task >= p.H_kv;
-        const int h = is_v ? task - p.H_kv : task;
+    for (int all = warp; all < look * p.H_kv; all += kRopeThreads / 32) {
+        const int which = all / p.H_kv, h = all % p.H_kv;
+        const int blk = blk_of[which];
+        if (blk < 0) continue;                               // another token leads that block
+        const unsigned have = __ballot_sync(0xffffffffu, lane < kBlock && tok_of[which][lane % kBlock] >= 0);
+        const size_t th = (size_t)blk * p.H_kv + h;
+        uint8_t* tile = (is_v ? p.v_pool : p.k_pool) + th * kBlock * RB;
+        float* scale = (is_v ? p.v_scale : p.k_scale) + th;
+        const float stored = *scale;                         // in flight with the rows
+        auto some = [&](int pass) { return (have >> (RPP * pass)) & ((1u << RPP) - 1u); };   // the pass has tokens
         const uint16_t* src = is_v ? p.v + h * D : p.k + h * D;
         const int64_t stride = is_v ? p.v_stride : p.k_stride;
         uint2 x[PASSES][2];
         float amax = 0.f;
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
-            const int o = tok_of[RPP * i + sub];
             x[i][0] = x[i][1] = make_uint2(0u, 0u);
+            const int o = tok_of[which][RPP * i + sub];
             if (o >= 0) {
                 x[i][0] = *reinterpret_cast<const uint2*>(src + o * stride + d0);
                 x[i][1] = *reinterpret_cast<const uint2*>(src + o * stride + d1);
@@ -218,11 +268,12 @@ __device__ __forceinline__ void quantize_block(const RopeParams& p, int t)
         }
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
-            const int o = tok_of[RPP * i + sub];
+            if (!some(i)) continue;
+            const int o = tok_of[which][RPP * i + sub];
             float2 a = unpack2<BF16>(x[i][0].x), b = unpack2<BF16>(x[i][0].y);
             float2 e = unpack2<BF16>(x[i][1].x), f = unpack2<BF16>(x[i][1].y);
             if (!is_v && rotated && o >= 0) {
-                const float* tab = p.table + (size_t)p.positions[o] * p.rot + 4 * ln;
+                const float* tab = p.table + (size_t)pos_of[which][RPP * i + sub] * p.rot + 4 * ln;
                 const float4 c = __ldg(reinterpret_cast<const float4*>(tab));
                 const float4 s = __ldg(reinterpret_cast<const float4*>(tab + half));
                 if (p.inter) {
@@ -248,24 +299,27 @@ __device__ __forceinline__ void quantize_block(const RopeParams& p, int t)
 #pragma unroll
         for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
 
-        const size_t th = (size_t)blk * p.H_kv + h;
-        uint8_t* tile = (is_v ? p.v_pool : p.k_pool) + th * kBlock * RB;
-        float* scale = (is_v ? p.v_scale : p.k_scale) + th;
-        const float s_old = first == 0 ? 0.f : *scale;       // offset 0 written: a fresh block
+        const float s_old = (have & 1u) ? 0.f : stored;      // offset 0 written: a fresh block
         const float s = fmaxf(s_old, __fdiv_rn(amax, quant_limit<DT>()));
         const bool grown = s > s_old && s_old > 0.f;
+        const float inv = __fdiv_rn(1.f, s);
+        const bool exact = !(inv < INFINITY);                // s 0 or tiny: a division per element
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
+            if (!grown && !some(i)) continue;
             const int off = RPP * i + sub;
             uint8_t* row = tile + off * RB;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const int d = r ? d1 : d0;
                 uint32_t w = 0;
-                if (tok_of[off] >= 0) {
+                if (tok_of[which][off] >= 0) {
                     const float2 a = unpack2<BF16>(x[i][r].x), b = unpack2<BF16>(x[i][r].y);
-                    w = pack_codes<DT>(quant_code<DT>(a.x, s), quant_code<DT>(a.y, s), quant_code<DT>(b.x, s),
-                                       quant_code<DT>(b.y, s));
+                    if (exact)
+                        w = pack_codes<DT>(quant_code<DT>(a.x, s), quant_code<DT>(a.y, s), quant_code<DT>(b.x, s),
+                                           quant_code<DT>(b.y, s));
+                    else
+                        w = quant_codes4<DT>({a.x, a.y, b.x, b.y}, s, inv);
                 } else if (grown) {
                     const uint32_t c = load_codes4<DT>(row, d);
                     w = pack_codes<DT>(requant_code<DT>(code_at<DT>(c, 0), s_old, s),
@@ -284,7 +338,7 @@ __device__ __forceinline__ void quantize_block(const RopeParams& p, int t)
 }
 
 template <int D, bool BF16, int DT>
-__global__ void __launch_bounds__(kRopeThreads) append_rope_kernel(const RopeParams p)
+__global__ void __launch_bounds__(kRopeThreads, 4) append_rope_kernel(const RopeParams p)
 {
     if ((int)blockIdx.x < p.copy_ctas) {
         copy_rows<D, BF16>(p, blockIdx.x);
@@ -292,7 +346,8 @@ __global__ void __launch_bounds__(kRopeThreads) append_rope_kernel(const RopePar
     }
     if constexpr (DT == PKV_INT8 || DT == PKV_INT4 || DT == PKV_FP8E4M3) {
         if (p.index) pdl_wait_primary();   // the slots' tokens, written by the kernel before this one
-        quantize_block<D, BF16, DT>(p, blockIdx.x - p.copy_ctas);
+        const int cta = (int)blockIdx.x - p.copy_ctas;
+        quantize_block<D, BF16, DT>(p, cta >> 1, cta & 1);
     }
 }
 
@@ -371,7 +426,8 @@ int launch_append_rope(const AppendArgs& a, const RopeArgs& r, cudaStream_t s)
     p.copy_y = a.T <= 2 * num_sms() ? (p.rows + step - 1) / step : 1;
     if (p.copy_y < 1) p.copy_y = 1;
     p.copy_ctas = p.rows > 0 ? a.T * p.copy_y : 0;
-    const unsigned grid = (unsigned)p.copy_ctas + (quant ? (unsigned)a.T : 0u);
+    // quantizing: a CTA for K and one for V of every token, or every kLook tokens
+    const unsigned grid = (unsigned)p.copy_ctas + (!quant ? 0u : 2u * (indexed ? (unsigned)((a.T + kLook - 1) / kLook) : (unsigned)a.T));
     if (indexed) {
         append_rope_index_kernel<<<(unsigned)((a.T + 255) / 256), 256, 0, s>>>(p);
         if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;

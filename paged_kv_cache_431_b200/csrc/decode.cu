@@ -77,6 +77,7 @@ decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
     RaggedItem it;
     const int32_t* trow;
     if constexpr (RAG) {
+        if (ragged_beside(p.rg)) return;
         it = ragged_item(p.rg, p.ctx_lens, p.W, p.max_parts * p.part_tokens, b, p.status,
                          threadIdx.x == 0 && part == 0 && blockIdx.y == 0);
         GC = min(16, it.rows * p.G - 16 * hg);   // query rows of this warp; none: it only helps
@@ -195,6 +196,7 @@ decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
     const float sl = p.scale_log2;
 
+    [[maybe_unused]] const bool upper = GC > 8;   // query rows 8 .. 15 of this warp
     int j = 0;
     bool ok = true;
     for (; j < ntiles; ++j) {
@@ -229,8 +231,10 @@ decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
         // online softmax, rows r (c = 0, 1) and r + 8 (c = 2, 3)
         float pr[2][4];
         float alpha[2];
+        if constexpr (RAG) alpha[0] = alpha[1] = 1.f;
 #pragma unroll
         for (int hr = 0; hr < NHT; ++hr) {
+            if (RAG && hr == 1 && !upper) continue;   // items of up to 8 query rows: no upper half
             float x[2][2];
             float mx = -INFINITY;
 #pragma unroll
@@ -276,7 +280,8 @@ decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
         // P^T as the B operand of O^T += V^T . P^T (k = tokens, n = heads), hi + lo parts
         uint32_t bh[NHT][2], bl[NHT][2];
 #pragma unroll
-        for (int hn = 0; hn < NHT; ++hn)
+        for (int hn = 0; hn < NHT; ++hn) {
+            if (RAG && hn == 1 && !upper) continue;
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
                 const float p0 = pr[nt][2 * hn], p1 = pr[nt][2 * hn + 1];
@@ -286,6 +291,7 @@ decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
                     bl[hn][nt] = pack2<BF16>(p0 - back.x, p1 - back.y);
                 }
             }
+        }
 
         uint32_t keep01 = 0xffffffffu, keep23 = 0xffffffffu;
         if (nv < kBlock || nlo > 0) {   // zero V outside [nlo, nv): P is 0 there, V may be stale
@@ -303,6 +309,7 @@ decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
             va[3] &= keep23;
 #pragma unroll
             for (int hn = 0; hn < NHT; ++hn) {
+                if (RAG && hn == 1 && !upper) continue;
                 mma16816<BF16>(o[mt][hn], va, bh[hn][0], bh[hn][1]);
                 if constexpr (!RAG) mma16816<BF16>(o[mt][hn], va, bl[hn][0], bl[hn][1]);
             }
@@ -638,6 +645,22 @@ template <typename K>
 int launch_k(K kernel, int smem, dim3 grid, int threads, cudaStream_t s, const DecodeParams& p,
              const CUtensorMap* tmk, const CUtensorMap* tmv)
 {
+    if (p.rg.beside) {   // scheduled while the prefix pass runs (ragged_beside in the kernel)
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+            cudaLaunchKernelEx(&cfg, kernel, p, *tmk, *tmv) != cudaSuccess)
+            return PKV_ERR_CUDA;
+        return PKV_OK;
+    }
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return PKV_ERR_CUDA;
     kernel<<<grid, threads, smem, s>>>(p, *tmk, *tmv);
@@ -673,7 +696,7 @@ int launch_mma16(const DecodeParams& p, int nht, dim3 grid, cudaStream_t s, cons
 
 int launch_decode(const DecodeArgs& a, const CUtensorMap* tmk, const CUtensorMap* tmv, cudaStream_t s)
 {
-    DecodeParams p;
+    DecodeParams p = {};
     p.q = a.q;
     p.tables = a.tables;
     p.ctx_lens = a.ctx_lens;
@@ -796,6 +819,7 @@ static DecodeParams ragged_params(const RaggedArgs& a)
     p.rg.max_prefix = a.max_prefix;
     p.rg.pre_part = a.pre_part;
     p.rg.max_group = a.max_group;
+    p.rg.beside = a.beside;
     p.rg.out16 = a.out;
     return p;
 }
@@ -803,7 +827,7 @@ static DecodeParams ragged_params(const RaggedArgs& a)
 int launch_ragged_short(const RaggedArgs& a, const CUtensorMap* tmk, const CUtensorMap* tmv, cudaStream_t s)
 {
     const DecodeParams p = ragged_params(a);
-    const dim3 grid(a.max_parts, a.H_kv * p.hgroups, a.items);
+    const dim3 grid(a.max_parts, a.H_kv * p.hgroups, a.items + (a.beside ? 1 : 0));
     const int nht = a.max_rows * a.G <= 8 ? 1 : 2;
     if (is_quantized(a.kv_dtype)) return launch_decode_quant_ragged(p, a.kv_dtype, a.d, nht, grid, s, tmk, tmv);
     const bool bf = a.kv_dtype == PKV_BF16;

@@ -37,6 +37,7 @@ struct RaggedParams {
     int max_prefix;               // kPrefix, kSuffix: tokens of a prefix that the grid covers
     int pre_part;                 // kSuffix's merge: tokens per prefix partition
     int max_group;                // kSuffix: sequences of a group that the prefix pass covered
+    int beside;                   // launched to run beside the kernel before it
     void* out16;                  // [total_rows][H_q][d] of q's dtype
 };
 
@@ -177,6 +178,17 @@ __device__ __forceinline__ RaggedItem ragged_item(const RaggedParams& r, const i
         it.end = it.end < it.base ? it.base : cap;
     }
     return it;
+}
+
+// The suffix pass of a grouped decode is launched to run beside its prefix pass (neither needs the
+// other), and the merge after it waits only for its primary, the suffix grid.  So that grid has one
+// more item, whose first block does nothing but wait for the prefix grid: the suffix grid is then
+// complete only after the prefix grid is, its partials visible.  True for blocks of that item.
+__device__ __forceinline__ bool ragged_beside(const RaggedParams& r)
+{
+    if (!r.beside || blockIdx.z != gridDim.z - 1) return false;
+    if ((blockIdx.x | blockIdx.y) == 0) pdl_wait_primary();
+    return true;
 }
 
 // Index (in rows of H_q heads, flattened) of the item's query row n of KV head g.

@@ -288,6 +288,7 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
     RaggedItem it;
     const int32_t* trow;
     if constexpr (RAG) {
+        if (ragged_beside(p.rg)) return;
         it = ragged_item(p.rg, p.ctx_lens, p.W, p.max_parts * p.part_tokens, b, p.status,
                          lane == 0 && part == 0 && blockIdx.y == 0);
         GC = min(16, it.rows * p.G - 16 * hg);   // query rows of this CTA
@@ -489,6 +490,7 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
             for (int c = 0; c < 4; ++c) o[mt][hn][c] = 0.f;
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
 
+    [[maybe_unused]] const bool upper = GC > 8;   // query rows 8 .. 15 of this CTA
     int j = 0;
     bool ok = true;
     for (; j < ntiles; ++j) {
@@ -538,8 +540,10 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
         const float sl = p.scale_log2 * sc_kv.x;
         float pr[2][4];
         float alpha[2];
+        if constexpr (RAG) alpha[0] = alpha[1] = 1.f;
 #pragma unroll
         for (int hr = 0; hr < NHT; ++hr) {
+            if (RAG && hr == 1 && !upper) continue;   // items of up to 8 query rows: no upper half
             float x[2][2];
             float mx = -INFINITY;
             const float cb = SUBN ? qoff[hr] * sl : 0.f;
@@ -595,7 +599,8 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
         // P^T (times the tile's V scale) as fp16 hi + lo B fragments
         uint32_t bh[NHT][2], bl[NHT][2];
 #pragma unroll
-        for (int hn = 0; hn < NHT; ++hn)
+        for (int hn = 0; hn < NHT; ++hn) {
+            if (RAG && hn == 1 && !upper) continue;
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
                 const float p0 = pr[nt][2 * hn] * sc_kv.y, p1 = pr[nt][2 * hn + 1] * sc_kv.y;
@@ -605,6 +610,7 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
                     bl[hn][nt] = pack2<false>(p0 - back.x, p1 - back.y);
                 }
             }
+        }
 
         uint32_t keep01 = 0xffffffffu, keep23 = 0xffffffffu;
         const bool partial = !whole;
@@ -634,6 +640,7 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
                 }
 #pragma unroll
                 for (int hn = 0; hn < NHT; ++hn) {
+                    if (RAG && hn == 1 && !upper) continue;
                     mma16816<false>(o[mt][hn], va[jj], bh[hn][0], bh[hn][1]);
                     if constexpr (!RAG) mma16816<false>(o[mt][hn], va[jj], bl[hn][0], bl[hn][1]);
                 }
@@ -739,6 +746,19 @@ int launch_q(const DecodeParams& p, int nht, dim3 grid, cudaStream_t s, const CU
     auto kern = nht == 1 ? k1 : k2;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return PKV_ERR_CUDA;
+    if (p.rg.beside) {   // scheduled while the prefix pass runs (ragged_beside in the kernel)
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(32);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, kern, p, *tmk, *tmv) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    }
     kern<<<grid, 32, smem, s>>>(p, *tmk, *tmv);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

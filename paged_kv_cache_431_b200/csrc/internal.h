@@ -163,6 +163,7 @@ struct RaggedArgs {
     int part_tokens, max_parts;
     int part_base, slots;   // first workspace slot of this launch, slots per row
     int max_prefix, pre_part, max_group;
+    int beside;             // run beside the launch before it (a suffix pass beside its prefix pass)
     float scale;
     const float* k_scale;
     const float* v_scale;

@@ -86,4 +86,42 @@ __device__ __forceinline__ void store_codes4(uint8_t* row, int d, uint32_t w)
     else *reinterpret_cast<uint32_t*>(row + d) = w;
 }
 
+// The packed codes of four elements over a scale s that they share, without four divisions.  With
+// inv = fl(1 / s), r = fl(x inv) is off the rounded quotient fl(x / s) by less than 2^-22 of it (three
+// roundings of 2^-24), and the code is a monotonic function of the quotient: so where the codes of
+// r (1 - 2^-22) and r (1 + 2^-22) agree, that is the code; where one of the four does not (a quotient
+// next to a border, a NaN), the divisions decide.  inv must be finite, and |x| <= s * the limit for
+// finite x, so that no clamp is needed.
+template <int DT>
+__device__ __forceinline__ uint32_t quant_codes4(const float (&x)[4], float s, float inv)
+{
+    float r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __fmul_rn(x[i], inv);
+    constexpr float LO = 1.f - 0x1p-22f, HI = 1.f + 0x1p-22f;
+    uint32_t w;
+    bool same;
+    if constexpr (DT == PKV_FP8E4M3) {
+        auto pair = [](float a, float b) -> uint32_t {
+            return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+        };
+        w = pair(r[0] * LO, r[1] * LO) | (pair(r[2] * LO, r[3] * LO) << 16);
+        same = w == (pair(r[0] * HI, r[1] * HI) | (pair(r[2] * HI, r[3] * HI) << 16));
+    } else {
+        // the nearest integer in the low bits of r + 1.5 x 2^23
+        constexpr float M = 12582912.f;
+        uint32_t n[4];
+        same = true;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float lo = __fmaf_rn(r[i], LO, M), hi = __fmaf_rn(r[i], HI, M);
+            same = same && lo == hi;
+            n[i] = __float_as_uint(lo) & (DT == PKV_INT8 ? 0xffu : 0xfu);
+        }
+        w = pack_codes<DT>(n[0], n[1], n[2], n[3]);
+    }
+    if (same) return w;
+    return pack_codes<DT>(quant_code<DT>(x[0], s), quant_code<DT>(x[1], s), quant_code<DT>(x[2], s), quant_code<DT>(x[3], s));
+}
+
 }  // namespace pkv

@@ -12,7 +12,7 @@
 //          rows against two key partitions, each with its own K/V tiles; both write partials.
 // Warps: 0..3 and 4..7 are the softmax of A and B (one thread per query row = TMEM lane), 8 and 10
 // fetch K and V (TMA, one box per paged block), 9 and 11 issue the MMAs of A and B; for quantized pools
-// 12..15 turn fetched code tiles into fp16 tiles (the codes are exact in fp16; the K scale of a (block,
+// 12.. turn fetched code tiles into fp16 tiles (the codes are exact in fp16; the K scale of a (block,
 // head) multiplies its 16 scores, its V scale multiplies P, so a tile is converted once for all
 // rows).  Per key tile and query tile: S (128 columns of TMEM) -> P back over the same columns as
 // 16-bit pairs, the A operand of P.V, in two halves of 64 keys so that P.V starts while the other
@@ -59,11 +59,16 @@ struct Cfg {
     static constexpr int NS = QUANT ? 2 : (D == 64 ? 4 : PAIR ? 3 : 2);
     static constexpr int NC = QUANT ? (PAIR || D == 64 ? 2 : DT == PKV_INT4 ? 2 : 1) : 1;
     static constexpr int SMEM = QT * TILE + NS * 2 * TILE + NC * 2 * CTILE + 1024;
-    static constexpr int THREADS = QUANT ? 512 : 384;
-    // registers of a softmax thread: a row's 128 scores stay in them.  The block is launched with
-    // THREADS x 168 (quantized: 128) and gives what the other warpgroups release: 2 x 216 + 72 =
-    // 3 x 168; 2 x 168 + 72 + 96 <= 4 x 128.
-    static constexpr int SOFTMAX_REGS = QUANT ? 168 : 216;
+    static constexpr int CONV = PAIR ? 4 : 2;                     // converter warps for K, and for V (quantized pools)
+    static constexpr int THREADS = QUANT ? 384 + 64 * CONV : 384;
+    // A softmax thread keeps its row's 128 scores in registers, but for the PAIR form of quantized
+    // pools: there eight converter warps are worth more (fp8, 48 rows against 4 x 32,768 keys: 169 ->
+    // 150 us; with shared tiles, where a tile is converted for 256 rows, 785 -> 813 us).  The block is
+    // launched with 168, 128 or 96 a thread, and the softmax warpgroups take what the others release:
+    // 2 x 216 + 72 = 3 x 168;  2 x 168 + 72 + 96 <= 4 x 128;  2 x 136 + 56 + 2 x 72 <= 5 x 96.
+    static constexpr bool ONE_PASS = !QUANT || !PAIR;
+    static constexpr int SOFTMAX_REGS = !QUANT ? 216 : PAIR ? 136 : 168;
+    static constexpr int ISSUE_REGS = QUANT && PAIR ? 56 : 72, CONV_REGS = PAIR ? 72 : 96;
     static constexpr int SWZ = ROW >= 128 ? 7 : ROW == 64 ? 3 : 1;   // TMA swizzle of a code tile
     static_assert(SMEM <= 225 * 1024, "dynamic shared memory, with 2 KB left for the static part");
 };
@@ -244,20 +249,20 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
         s_vmax = 0;
         s_armed[0] = s_armed[1] = 0;
         for (int s = 0; s < NS; ++s) {
-            mbar_init(smem_u32(&bars.k_full[s]), C::QUANT ? 2 : 1);
+            mbar_init(smem_u32(&bars.k_full[s]), C::QUANT ? C::CONV : 1);
             mbar_init(smem_u32(&bars.k_empty[s]), shared ? 2 : 1);
-            mbar_init(smem_u32(&bars.v_full[s]), C::QUANT ? 2 : 1);
+            mbar_init(smem_u32(&bars.v_full[s]), C::QUANT ? C::CONV : 1);
             mbar_init(smem_u32(&bars.v_empty[s]), shared ? 2 : 1);
         }
         if constexpr (C::QUANT) {
             for (int s = 0; s < NC; ++s) {
                 mbar_init(smem_u32(&bars.ck_full[s]), 1);
-                mbar_init(smem_u32(&bars.ck_empty[s]), 2);
+                mbar_init(smem_u32(&bars.ck_empty[s]), C::CONV);
                 mbar_init(smem_u32(&bars.cv_full[s]), 1);
-                mbar_init(smem_u32(&bars.cv_empty[s]), 2);
+                mbar_init(smem_u32(&bars.cv_empty[s]), C::CONV);
             }
             for (int s = 0; s < kScaleSlots; ++s) {
-                mbar_init(smem_u32(&bars.sc_full[s]), 2);
+                mbar_init(smem_u32(&bars.sc_full[s]), C::CONV);
                 mbar_init(smem_u32(&bars.sc_empty[s]), shared ? 8 : 4);
             }
         }
@@ -404,36 +409,51 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 if (!ok) break;
             }
             tc_fence_after();
-            // the row's 128 scores, kept in registers from here to P
-            float v[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, v[c]);
             // per paged block of 16 keys (quantized pools): (K, V) scales, read where they are needed
             const float2* sc = s_scale + (C::QUANT ? (n % kScaleSlots) * kBlocks : 0);
             const int left = hi - lo - t * kBN;                   // keys of this tile in the range
             const bool need_mask = left < kBN;
-            tmem_wait_ld();
-            if (need_mask) {
+            // the row's 128 scores: kept in registers from here to P, or read twice, 32 at a time
+            float v[C::ONE_PASS ? 4 : 1][32];
+            if constexpr (C::ONE_PASS) {
 #pragma unroll
-                for (int j = 0; j < kBN; ++j)
-                    if (j >= left) v[j >> 5][j & 31] = -INFINITY;
+                for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, v[c]);
+                tmem_wait_ld();
+                if (need_mask) {
+#pragma unroll
+                    for (int j = 0; j < kBN; ++j)
+                        if (j >= left) v[j >> 5][j & 31] = -INFINITY;
+                }
             }
             // the row maximum of the scaled scores, in three-input maxima per paged block
-            float m8[kBlocks];
+            float mx = -INFINITY;
 #pragma unroll
-            for (int b8 = 0; b8 < kBlocks; ++b8) {
-                const float* w = &v[b8 >> 1][16 * (b8 & 1)];
-                float m0 = fmax3(w[0], w[1], w[2]), m1 = fmax3(w[3], w[4], w[5]);
-                m0 = fmax3(m0, w[6], w[7]);
-                m1 = fmax3(m1, w[8], w[9]);
-                m0 = fmax3(m0, w[10], w[11]);
-                m1 = fmax3(m1, w[12], w[13]);
-                m8[b8] = fmax3(m0, w[14], w[15]);
-                m8[b8] = fmaxf(m8[b8], m1);
-                // a block of scale 0 must not turn a masked -inf into NaN: its scores are 0
-                if constexpr (C::QUANT) m8[b8] = m8[b8] == -INFINITY ? m8[b8] : m8[b8] * (sl * sc[b8].x);
+            for (int c = 0; c < 4; ++c) {
+                float* w = v[C::ONE_PASS ? c : 0];
+                if constexpr (!C::ONE_PASS) {
+                    tmem_ld32(tS + 32 * c, v[0]);
+                    tmem_wait_ld();
+                    if (need_mask) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (32 * c + j >= left) w[j] = -INFINITY;
+                    }
+                }
+                float m2[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float* u = w + 16 * k;
+                    float m0 = fmax3(u[0], u[1], u[2]), m1 = fmax3(u[3], u[4], u[5]);
+                    m0 = fmax3(m0, u[6], u[7]);
+                    m1 = fmax3(m1, u[8], u[9]);
+                    m0 = fmax3(m0, u[10], u[11]);
+                    m1 = fmax3(m1, u[12], u[13]);
+                    m2[k] = fmaxf(fmax3(m0, u[14], u[15]), m1);
+                    // a block of scale 0 must not turn a masked -inf into NaN: its scores are 0
+                    if constexpr (C::QUANT) m2[k] = m2[k] == -INFINITY ? m2[k] : m2[k] * (sl * sc[2 * c + k].x);
+                }
+                mx = fmax3(mx, m2[0], m2[1]);
             }
-            float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
             if constexpr (!C::QUANT) mx = mx == -INFINITY ? mx : mx * sl;
             float m_new = m_used;
             if (mx > m_used + kSlack || m_used == -INFINITY) m_new = mx;
@@ -482,6 +502,11 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
 #pragma unroll
                 for (int cc = 0; cc < 2; ++cc) {
                     const int c = 2 * half + cc;
+                    const float* u = v[C::ONE_PASS ? c : 0];
+                    if constexpr (!C::ONE_PASS) {
+                        tmem_ld32(tS + 32 * c, v[0]);
+                        tmem_wait_ld();
+                    }
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
@@ -492,7 +517,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                             f = sl * kv.x;
                             vm = v_mul * kv.y;
                         }
-                        float2 a = ffma2(make_float2(v[c][2 * e], v[c][2 * e + 1]), make_float2(f, f), mref2);
+                        float2 a = ffma2(make_float2(u[2 * e], u[2 * e + 1]), make_float2(f, f), mref2);
                         if constexpr (decltype(masked)::value) {   // again: -inf times a factor of 0 is NaN
                             if (32 * c + 2 * e >= left) a.x = -INFINITY;
                             if (32 * c + 2 * e + 1 >= left) a.y = -INFINITY;
@@ -564,7 +589,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
             }
         }
     } else if (warp < 12) {
-        regs_dec<72>();
+        regs_dec<C::ISSUE_REGS>();
         if (warp == 8 || warp == 10) {
         // ------------------------------------------------------------ producers (8: K, 10: V)
         // The lanes hold the block ids of the next 4 key tiles of A and of B (one load per 4 tiles,
@@ -688,13 +713,13 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
         mbar_wait_bounded(smem_u32(&bars.mma_drain[x]), 0, p.wait_cycles);
         }
     } else if constexpr (C::QUANT) {
-        regs_dec<96>();
+        regs_dec<C::CONV_REGS>();
         // ------------------------------------------------------------ converters
-        // Warps 12 and 13 convert K tiles, 14 and 15 V tiles, each at the pace of its ring.  A thread
-        // takes two keys of a tile: a row of codes -> a row of the fp16 tile (both swizzled by 16-byte
-        // chunks, so the 32 rows of a warp spread over the banks).
-        const bool is_v = warp >= 14;
-        const int id = threadIdx.x & 63;
+        // The first CONV warps convert K tiles, the others V tiles, each at the pace of its ring.  A
+        // thread takes one key of a tile (or two): its row of codes -> its row of the fp16 tile (both
+        // swizzled by 16-byte chunks, so the 32 rows of a warp spread over the banks).
+        const bool is_v = warp >= 12 + C::CONV;
+        const int id = (int)threadIdx.x - 384 - (is_v ? 32 * C::CONV : 0);
         auto convert = [&](uint32_t code, uint32_t dst, int key, bool zero) {
             const int base = key * C::ROW;
             const int sw = (base >> 7) & C::SWZ;
@@ -753,8 +778,8 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 if (id == 0) s_armed[is_v ? 1 : 0] = n + 1;
                 if (!is_v && id < kBlocks) s_scale[(n % kScaleSlots) * kBlocks + id] = mine;
 #pragma unroll 1
-                for (int k = 0; k < 2; ++k)
-                    convert(from + cs * C::CTILE, to + s * TILE, id + 64 * k, is_v && id + 64 * k >= left);
+                for (int key = id; key < kBN; key += 32 * C::CONV)
+                    convert(from + cs * C::CTILE, to + s * TILE, key, is_v && key >= left);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {

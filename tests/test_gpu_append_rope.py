@@ -231,3 +231,34 @@ def test_rope_in_place_other_stream_and_graph():
     torch.cuda.synchronize()
     same_pool(pool, before, 1)
     assert pkv.read_device_status(pool) == 0
+
+
+@pytest.mark.parametrize("dt", pkv.QUANTIZED, ids=lambda x: NAMES[x])
+@pytest.mark.parametrize("gain", [1e-38, 1e-3, 1.0, 1e30])
+def test_rope_append_codes_at_rounding_borders(dt, gain):
+    """Values that are codes, or halfway between codes, of the tile's scale, from the smallest
+    magnitudes (whose reciprocal scale overflows) to large ones: the codes stay those of the division."""
+    g = wl.generator(3700)
+    T, H_kv, d, N = 48, 2, 128, 8
+    limit = {pkv.INT8: 127, pkv.INT4: 7, pkv.FP8E4M3: 448}[dt]
+    steps = torch.randint(-2 * limit, 2 * limit + 1, (T, H_kv, d), generator=g).float() / 2
+    steps[:, :, 0] = limit
+    k, v = (steps * gain).to(torch.bfloat16), (steps.flip(0) * gain).to(torch.bfloat16)
+    pool = stale_pool(N, H_kv, d, dt, g)
+    pool.k_scale.fill_(1e-39 * min(gain, 1.0))
+    pool.v_scale.fill_(1e-39 * min(gain, 1.0))
+    opool = oracle_copy(pool)
+    slots = torch.randperm(N * 16, generator=g)[:T].to(torch.int32)
+    cs = torch.zeros(1, 128)
+    cs[:, :64] = 1                                # a rotation by 0
+    pkv.kv_append_rope(pool, 0, None, k.to(DEV), v.to(DEV), torch.zeros(T, dtype=torch.int32, device=DEV), cs.to(DEV),
+                       slots.to(DEV))
+    torch.cuda.synchronize()
+    oracle.kv_append(opool, k, v, pkv.BF16, slots.numpy())
+    same_pool(pool, opool)
+
+
+@pytest.mark.parametrize("dt", [pkv.BF16, pkv.INT8], ids=lambda x: NAMES[x])
+def test_rope_append_many_single_tokens(dt):
+    """A wide decode step: every token in a block of its own (each block's first token leads alone)."""
+    run_case(dt, pkv.BF16, 64, 64, True, 1030, 1, 8, 2, True, 3800 + dt)
