@@ -69,6 +69,9 @@ struct Cfg {
     static constexpr bool ONE_PASS = !QUANT || !PAIR;
     static constexpr int SOFTMAX_REGS = !QUANT ? 216 : PAIR ? 136 : 168;
     static constexpr int ISSUE_REGS = QUANT && PAIR ? 56 : 72, CONV_REGS = PAIR ? 72 : 96;
+    // Head dim 64 leaves 64 columns of TMEM per tile, which hold P apart from S: S(t+1) is computed
+    // as soon as S(t) is in registers, beside the exponentials (else only after P(t).V).
+    static constexpr bool P_APART = D == 64 && ONE_PASS;
     static constexpr int SWZ = ROW >= 128 ? 7 : ROW == 64 ? 3 : 1;   // TMA swizzle of a code tile
     static_assert(SMEM <= 225 * 1024, "dynamic shared memory, with 2 KB left for the static part");
 };
@@ -87,6 +90,7 @@ struct Bars {
     uint64_t ck_full[2], ck_empty[2], cv_full[2], cv_empty[2];   // code tiles
     uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];        // the scales of a key tile
     uint64_t s_full[2];        // S(x, t) is in TMEM, and every earlier MMA of the CTA is done
+    uint64_t s_empty[2], pv_done[2];   // P_APART: S(x, t) is in registers; P.V(x, t) is done
     uint64_t p_full[2][2];     // a half of P(x, t) is stored
     uint64_t o_done[2];
     uint64_t mma_drain[2];
@@ -268,6 +272,8 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(smem_u32(&bars.s_full[x]), 1);
+            mbar_init(smem_u32(&bars.s_empty[x]), 4);
+            mbar_init(smem_u32(&bars.pv_done[x]), 1);
             mbar_init(smem_u32(&bars.p_full[x][0]), 4);
             mbar_init(smem_u32(&bars.p_full[x][1]), 4);
             mbar_init(smem_u32(&bars.o_done[x]), 1);
@@ -389,7 +395,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
         const int nx = x == 0 ? nA : nB;
         const int lo = key_lo(x), hi = key_hi(x);
         const uint32_t tS = tmem + ((uint32_t)(quarter * 32) << 16) + 256 * x;
-        const uint32_t tO = tS + 128;
+        const uint32_t tO = tS + 128, tP = C::P_APART ? tS + 192 : tS;
         float sl = fabsf(p.scale_log2);
         float v_unit = 1.f, v_mul = 1.f;
         if constexpr (C::QUANT) {
@@ -419,6 +425,11 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, v[c]);
                 tmem_wait_ld();
+                if constexpr (C::P_APART) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bars.s_empty[x]));
+                }
                 if (need_mask) {
 #pragma unroll
                     for (int j = 0; j < kBN; ++j)
@@ -459,7 +470,12 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
             if (mx > m_used + kSlack || m_used == -INFINITY) m_new = mx;
             const float alpha = m_used == -INFINITY ? 0.f : ex2(m_used - m_new);
             const float mref = m_new == -INFINITY ? 0.f : m_new;
-            // the max moved: rescale this row of O (P.V(t-1) is done: s_full(t) says so)
+            // the max moved: rescale this row of O (P.V(t-1) is done: s_full(t) says so, or pv_done)
+            if constexpr (C::P_APART) {
+                if (t > 0) ok = wait(bars.pv_done[x], (t - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+            }
             if (t > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
@@ -531,7 +547,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                         if constexpr (C::QUANT) pp = fmul2(pp, make_float2(vm, vm));
                         w[e] = pack2<C::BF16>(pp.x, pp.y);
                     }
-                    tmem_st16u(tS + 16 * c, w);
+                    tmem_st16u(tP + 16 * c, w);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -666,7 +682,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
         const int nx = x == 0 ? nA : nB;
         const uint32_t id_qk = idesc_f16(C::BF16, false, kBM, kBN);
         const uint32_t id_pv = idesc_f16(C::BF16, true, kBM, D);
-        const uint32_t tS = tmem + 256 * x, tO = tS + 128;
+        const uint32_t tS = tmem + 256 * x, tO = tS + 128, tP = C::P_APART ? tS + 192 : tS;
         const uint64_t dq = sdesc_k128(sQ + (PAIR ? 0 : x) * TILE);
         const uint64_t dk = sdesc_k128_sbo(sK, KV<D>::GROUP), dv = sdesc_mn128_sbo(sV, KV<D>::HALF, KV<D>::GROUP);
         bool ok = true;
@@ -685,6 +701,14 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
         };
         if (nx > 0) scores(0);
         for (int t = 0; ok && t < nx; ++t) {
+            if constexpr (C::P_APART) {
+                if (t + 1 < nx) {
+                    ok = wait(bars.s_empty[x], t & 1);
+                    if (ok) tc_fence_after();
+                    if (ok) scores(t + 1);
+                    if (!ok) break;
+                }
+            }
             const int n = seq(x, t), s = n % NS;
             const uint64_t v0 = dv + (uint32_t)(s * (TILE >> 4));
             ok = wait_tile(1, bars.v_full, n);
@@ -696,13 +720,14 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {   // 16 keys: two 8-row groups of V
                     const int ks = 4 * half + k;
-                    umma_ts_w(tO, tS + 8 * ks, v0 + ((ks * 2 * KV<D>::GROUP) >> 4), id_pv, t > 0 || ks > 0);
+                    umma_ts_w(tO, tP + 8 * ks, v0 + ((ks * 2 * KV<D>::GROUP) >> 4), id_pv, t > 0 || ks > 0);
                 }
             }
             if (!ok) break;
             if (t + 1 < nx) {
+                if constexpr (C::P_APART) umma_commit_w(smem_u32(&bars.pv_done[x]));
                 umma_commit_w(smem_u32(&bars.v_empty[s]));
-                scores(t + 1);
+                if constexpr (!C::P_APART) scores(t + 1);
             } else {
                 umma_commit_w(smem_u32(&bars.o_done[x]));
                 umma_commit_w(smem_u32(&bars.v_empty[s]));
