@@ -687,8 +687,10 @@ constexpr int kShortRowsQuant = 32;
 // One-warp CTAs per SM that a small batch is split into: 6 against 24 took int8, R 8, 4 x 32,768 from 97
 // to 67 us and an 8-sequence step from 38 to 27.
 constexpr int kRaggedCtas = 6;
+constexpr int kTcFixed = 5;
 
-static RaggedSplit ragged_split(pkv_pool_t pool, int items, int max_rows, int G, int max_tokens)
+// sms: SMs that the launch may count on.
+static RaggedSplit ragged_split(pkv_pool_t pool, int items, int max_rows, int G, int max_tokens, int sms = num_sms())
 {
     RaggedSplit r;
     const bool quant = is_quantized(pool->d.kv_dtype);
@@ -706,14 +708,23 @@ static RaggedSplit ragged_split(pkv_pool_t pool, int items, int max_rows, int G,
         while (P >= 256 && ctas * ((max_tokens + P - 1) / P) < (long long)kRaggedCtas * num_sms()) P /= 2;
         r.part = P;
     } else {
-        // one CTA per SM: split the keys until two waves are full, in whole 128-key tiles, at
-        // least two of them per partition
+        // One CTA per SM and a fixed cost per CTA (its query tiles, TMEM, partials: about kTcFixed key
+        // tiles): the split of the keys, in whole 128-key tiles, that makes waves x (tiles + fixed)
+        // smallest.  Filling one wave instead of two took 128 rows against 4 x 32,768 keys from 117 to
+        // 103 us, 512 rows against 8,192 from 161 to 126.
         const long long ctas = (long long)items * H_kv * ((R + (r.pair ? 127 : 255)) / (r.pair ? 128 : 256));
-        long long parts = 2LL * num_sms() / (ctas > 0 ? ctas : 1);
-        parts = (parts < 1 ? 1 : parts) * (r.pair ? 2 : 1);
-        const long long most = (max_tokens + 255) / 256;
-        parts = parts > most ? (most < 1 ? 1 : most) : parts;
-        r.part = (int)((((long long)max_tokens + parts - 1) / parts + 127) / 128 * 128);
+        const int tiles = (int)(((long long)max_tokens + 127) / 128), per = r.pair ? 2 : 1;
+        long long best = -1;
+        int parts = per;
+        for (int k = 1; k <= 64 && (k == 1 || k * per * 2 <= tiles); ++k) {
+            const long long waves = (ctas * k + sms - 1) / sms;
+            const long long cost = waves * ((tiles + k * per - 1) / (k * per) + kTcFixed);
+            if (best < 0 || cost < best) {
+                best = cost;
+                parts = k * per;
+            }
+        }
+        r.part = (tiles + parts - 1) / parts * 128;
         if (r.part < 128) r.part = 128;
     }
     r.parts = max_tokens > 0 ? (int)(((long long)max_tokens + r.part - 1) / r.part) : 1;
@@ -825,6 +836,21 @@ int paged_cross_attn(pkv_pool_t pool, int layer, const void* q, int q_dtype, con
     return launch_ragged_merge(a, s);
 }
 
+// The prefix pass of a grouped decode: where the suffixes, which run beside it, weigh more (their
+// bytes at HBM rate against the prefix tiles at about 2 us each), it is split for half the SMs, so that
+// both run side by side (8 prompts of 4,000 tokens, 32 sequences of up to 500 more on each: 122 -> 108 us).
+static RaggedSplit prefix_split(pkv_pool_t pool, int num_groups, int max_group_size, int G, int max_prefix_len,
+                                int num_seqs, int max_suffix_len)
+{
+    const pkv_pool_desc& d = pool->d;
+    const double rows = (double)max_group_size * G;
+    const double tiles = (double)num_groups * d.num_kv_heads * ((rows + 255) / 256) * ((max_prefix_len + 127) / 128);
+    const double prefix_us = tiles * 2.2 / num_sms();
+    const double suffix_us = (double)num_seqs * max_suffix_len * d.num_kv_heads * 2 * pool->row_bytes / 6.5e6;
+    return ragged_split(pool, num_groups, max_group_size, G, max_prefix_len,
+                        suffix_us > prefix_us ? (num_sms() + 1) / 2 : num_sms());
+}
+
 size_t paged_decode_groups_workspace_bytes(pkv_pool_t pool, int num_seqs, int num_q_heads, int num_groups,
                                            int max_group_size, int max_prefix_len, int max_suffix_len)
 {
@@ -832,7 +858,8 @@ size_t paged_decode_groups_workspace_bytes(pkv_pool_t pool, int num_seqs, int nu
         max_group_size < 0 || max_prefix_len < 0 || max_suffix_len < 0)
         return 0;
     const int G = num_q_heads / pool->d.num_kv_heads;
-    const int pre = max_prefix_len > 0 ? ragged_split(pool, num_groups, max_group_size, G, max_prefix_len).parts : 0;
+    const int pre = max_prefix_len > 0 ? prefix_split(pool, num_groups, max_group_size, G, max_prefix_len, num_seqs,
+                                                      max_suffix_len).parts : 0;
     const int own = ragged_split(pool, num_seqs, 1, G, max_suffix_len).parts;
     return pre + own > 1 ? ragged_ws_bytes(pool, num_seqs, num_q_heads, pre + own) : 0;
 }
@@ -854,7 +881,8 @@ int paged_decode_attn_groups(pkv_pool_t pool, int layer, const void* q, int q_dt
     if (!block_tables || !context_lens || !group_starts || !prefix_lens) return PKV_ERR_NULL;
     RaggedArgs a = ragged_args(pool, layer, q, q_dtype, num_q_heads, scale, num_seqs, block_tables, block_table_width,
                                context_lens, group_starts, out);
-    const RaggedSplit pre = max_prefix_len > 0 ? ragged_split(pool, num_groups, max_group_size, a.G, max_prefix_len)
+    const RaggedSplit pre = max_prefix_len > 0 ? prefix_split(pool, num_groups, max_group_size, a.G, max_prefix_len,
+                                                              num_seqs, max_suffix_len)
                                                : RaggedSplit{false, false, PKV_BLOCK_SIZE, 0};
     const RaggedSplit own = ragged_split(pool, num_seqs, 1, a.G, max_suffix_len);
     const int slots = pre.parts + own.parts;
