@@ -684,9 +684,7 @@ struct RaggedSplit {
 //   86 against 166, 151 against 168, 204 against 170.
 constexpr int kShortRows16 = 16;
 constexpr int kShortRowsQuant = 32;
-// One-warp CTAs per SM that a small batch is split into: 6 against 24 took int8, R 8, 4 x 32,768 from 97
-// to 67 us and an 8-sequence step from 38 to 27.
-constexpr int kRaggedCtas = 6;
+constexpr int kRaggedSlots = 12, kShortFixed = 24;
 constexpr int kTcFixed = 5;
 
 // sms: SMs that the launch may count on.
@@ -697,15 +695,27 @@ static RaggedSplit ragged_split(pkv_pool_t pool, int items, int max_rows, int G,
     const long long R = (long long)max_rows * G;
     const int H_kv = pool->d.num_kv_heads;
     r.tc = R > (quant ? kShortRowsQuant : kShortRows16);
+    // small quantized launches of 17 .. 32 rows: latency counts (32 rows against 2,000 int8 tokens: 25
+    // against 20 us)
+    if (quant && R > 16 && (long long)items * H_kv * (((long long)max_tokens + 127) / 128) <= 4LL * num_sms()) r.tc = true;
     r.pair = r.tc && R <= 128;
     if (!r.tc) {
-        // ~256 (192) KiB of K + V per partition as in the plain decode, halved, down to 128 (192)
-        // tokens, only until every SM has kRaggedCtas one-warp CTAs: a partition's partials weigh R
-        // query rows, not G, so few long sequences are not cut as finely as there
+        // From ~256 (192) KiB of K + V per partition, as in the plain decode, halved down to 128 (192)
+        // tokens: the size that makes rounds x (16-token tiles + fixed) smallest, with about
+        // kRaggedSlots one-warp CTAs at work per SM, and a partition's prologue, partials and merge
+        // weighing about kShortFixed tiles.  Few long sequences stay coarse (int8, R 8, 4 x 32,768 tokens:
+        // 67 us at 768 tokens, 97 at 192), short suffixes are cut finely (110 of up to 700 tokens, head
+        // dim 64: a step of 45 us at 1,024 tokens, 33 at 128).
         int P = (quant ? 192 : 256) * 1024 / (2 * pool->row_bytes);
         P = P < 128 ? 128 : (P > 4096 ? 4096 : P);
-        const long long ctas = (long long)items * H_kv * ((R + 15) / 16);
-        while (P >= 256 && ctas * ((max_tokens + P - 1) / P) < (long long)kRaggedCtas * num_sms()) P /= 2;
+        const double ctas = (double)items * H_kv * ((R + 15) / 16), slots = (double)kRaggedSlots * sms;
+        auto cost = [&](int part) {
+            const double n = ctas * ((max_tokens + part - 1) / part) / slots;
+            const int longest = max_tokens < part ? max_tokens : part;
+            return (n < 1 ? 1 : n) * ((longest + 15) / 16 + kShortFixed);
+        };
+        for (int half = P / 2; half >= 128 && half % PKV_BLOCK_SIZE == 0; half /= 2)
+            if (cost(half) < cost(P)) P = half;
         r.part = P;
     } else {
         // One CTA per SM and a fixed cost per CTA (its query tiles, TMEM, partials: about kTcFixed key

@@ -391,25 +391,41 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
     int eqr[2] = {0, 0};   // int8: the same per query row (rows r and r + 8)
     {
         const bool bf = p.q_bf16;
-        const uint16_t* qr[2];
         const uint16_t* qh = static_cast<const uint16_t*>(p.q) + ((size_t)b * p.H_q + hbase) * D;
-        if constexpr (RAG) {   // the lane's two query rows
-            qr[0] = static_cast<const uint16_t*>(p.q) + (r < GC ? ragged_row(it, p.G, p.H_q, g, 16 * hg + r) : 0) * D;
-            qr[1] = static_cast<const uint16_t*>(p.q) + (r + 8 < GC ? ragged_row(it, p.G, p.H_q, g, 16 * hg + r + 8) : 0) * D;
-        } else {
-            qr[0] = qh + r * D;
-            qr[1] = qh + (r + 8) * D;
-        }
         auto as_float = [&](uint16_t u) -> float {
             return bf ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
         };
-        auto qv = [&](int hr, int dim) -> float { return as_float(__ldg(qr[hr] + dim)); };   // row r + 8 hr
+        // ragged form: the lane's D/4 dims from qd * (D/4) of its two query rows, in 16-byte loads
+        [[maybe_unused]] uint32_t qw[RAG ? 2 : 1][RAG ? D / 8 : 1];
+        if constexpr (RAG) {
+#pragma unroll
+            for (int hr = 0; hr < NHT; ++hr) {
+                const bool in = r + 8 * hr < GC;
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    static_cast<const uint16_t*>(p.q) +
+                    (in ? ragged_row(it, p.G, p.H_q, g, 16 * hg + r + 8 * hr) : 0) * D + qd * (D / 4));
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint4 u = in ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+                    qw[hr][4 * i] = u.x;
+                    qw[hr][4 * i + 1] = u.y;
+                    qw[hr][4 * i + 2] = u.z;
+                    qw[hr][4 * i + 3] = u.w;
+                }
+            }
+        }
+        // q of row r + 8 hr, dim qd * (D/4) + off
+        auto qv = [&](int hr, int off) -> float {
+            if constexpr (RAG) return as_float((uint16_t)(qw[hr][off >> 1] >> (16 * (off & 1))));
+            else return as_float(__ldg(qh + (r + 8 * hr) * D + qd * (D / 4) + off));
+        };
         const bool r0 = r < GC, r1 = (NHT == 2) && (r + 8 < GC);
         float qmax = 0.f;
         if constexpr (RAG) {
-            for (int i = 0; i < D / 4; ++i) {
-                if (r < GC) qmax = fmaxf(qmax, fabsf(qv(0, qd * (D / 4) + i)));
-                if (NHT == 2 && r + 8 < GC) qmax = fmaxf(qmax, fabsf(qv(1, qd * (D / 4) + i)));
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) {   // rows beyond GC are 0
+                qmax = fmaxf(qmax, fabsf(qv(0, i)));
+                if (NHT == 2) qmax = fmaxf(qmax, fabsf(qv(1, i)));
             }
         } else {
             for (int i = lane; i < GC * D; i += 32) qmax = fmaxf(qmax, fabsf(as_float(__ldg(qh + i))));
@@ -426,7 +442,7 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
                     const bool live = (reg & 1) ? (NHT == 2 && r + 8 < GC) : (r < GC);
 #pragma unroll
                     for (int jj = 0; jj < 4; ++jj)
-                        if (live) rm[reg & 1] = fmaxf(rm[reg & 1], fabsf(qv(reg & 1, qd * (D / 4) + 8 * ks + 4 * (reg >> 1) + jj)));
+                        if (live) rm[reg & 1] = fmaxf(rm[reg & 1], fabsf(qv(reg & 1, 8 * ks + 4 * (reg >> 1) + jj)));
                 }
 #pragma unroll
             for (int hr = 0; hr < 2; ++hr) {
@@ -442,7 +458,7 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
                     uint32_t w0 = 0u, w1 = 0u;
 #pragma unroll
                     for (int jj = 0; jj < 4; ++jj) {
-                        const int Q = live ? __float2int_rn(qv(reg & 1, qd * (D / 4) + 8 * ks + 4 * (reg >> 1) + jj) *
+                        const int Q = live ? __float2int_rn(qv(reg & 1, 8 * ks + 4 * (reg >> 1) + jj) *
                                                             pow2f(eqr[reg & 1]))
                                            : 0;
                         const int d1 = (Q + 128) >> 8;
@@ -455,8 +471,9 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
         }
 #pragma unroll
         for (int ks = 0; ks < (KI8 ? 0 : Cfg::KS); ++ks) {
-            const int d0 = kdim<DT, D>(ks, qd, 0), d1 = kdim<DT, D>(ks, qd, 1);
-            const int d2 = kdim<DT, D>(ks, qd, 2), d3 = kdim<DT, D>(ks, qd, 3);
+            // dims of the k-slots, counted from the lane's first, qd * (D/4)
+            const int d0 = kdim<DT, D>(ks, 0, 0), d1 = kdim<DT, D>(ks, 0, 1);
+            const int d2 = kdim<DT, D>(ks, 0, 2), d3 = kdim<DT, D>(ks, 0, 3);
             qa[ks][0] = r0 ? pack2<false>(qv(0, d0) * qs, qv(0, d1) * qs) : 0u;
             qa[ks][2] = r0 ? pack2<false>(qv(0, d2) * qo, qv(0, d3) * qo) : 0u;
             qa[ks][1] = r1 ? pack2<false>(qv(1, d0) * qs, qv(1, d1) * qs) : 0u;
