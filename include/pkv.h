@@ -334,7 +334,8 @@ PKV_API size_t paged_decode_groups_workspace_bytes(pkv_pool_t pool, int num_seqs
  * for the rows of its whole group, each sequence's other tokens on their own, and both are merged
  * with the log-sum-exp rule; the result is the attention over the whole context.
  *   q, out [device]: [num_seqs][num_q_heads][head_dim], both of q_dtype (PKV_F16 or PKV_BF16; for
- *        16-bit pools the pool dtype), 16-byte aligned.  Sums and softmax are fp32, rounded once.
+ *        16-bit pools the pool dtype), 16-byte aligned, not overlapping.  Sums and softmax are
+ *        fp32, rounded once.
  *   block_tables, context_lens [device]: as paged_decode_attn; every sequence's table starts with
  *        its group's prefix blocks, and its context is at least the prefix.
  *   group_starts [device]: int32 [num_groups + 1], ascending: group g is the sequences
@@ -369,7 +370,8 @@ PKV_API size_t paged_cross_workspace_bytes(pkv_pool_t pool, int total_rows, int 
  * Rows of one sequence may be the tokens of a prompt, one token, or the hypotheses of a beam.
  * A context length of 0 gives zero rows.
  *   q, out [device]: [total_rows][num_q_heads][head_dim], both of q_dtype (PKV_F16 or PKV_BF16;
- *        for 16-bit pools the pool dtype), 16-byte aligned.  Sums and softmax are fp32, rounded once.
+ *        for 16-bit pools the pool dtype), 16-byte aligned, not
+ *        overlapping.  Sums and softmax are fp32, rounded once.
  *   row_starts [device]: int32 [num_seqs + 1], ascending, in [0, total_rows].  A sequence may have
  *        no rows; rows of no sequence (behind the last) are padding, their output is left as it is.
  *   block_tables, context_lens [device]: as paged_decode_attn.

@@ -726,7 +726,7 @@ static RaggedSplit ragged_split(pkv_pool_t pool, int items, int max_rows, int G,
         const int tiles = (int)(((long long)max_tokens + 127) / 128), per = r.pair ? 2 : 1;
         long long best = -1;
         int parts = per;
-        for (int k = 1; k <= 64 && (k == 1 || k * per * 2 <= tiles); ++k) {
+        for (int k = 1; k <= 64 && (k == 1 || (k * per * 2 <= tiles && (long long)items * k <= 65535)); ++k) {
             const long long waves = (ctas * k + sms - 1) / sms;
             const long long cost = waves * ((tiles + k * per - 1) / (k * per) + kTcFixed);
             if (best < 0 || cost < best) {
@@ -755,7 +755,7 @@ static size_t ragged_ws_bytes(pkv_pool_t pool, int rows, int num_q_heads, int sl
     return (size_t)rows * num_q_heads * slots * (pool->d.head_dim + 2) * sizeof(float);
 }
 
-// The checks that both ragged calls share.  PKV_OK with *empty set: nothing to do.
+// The checks that both ragged calls share.
 static int ragged_checks(pkv_pool_t pool, int layer, const void* q, int q_dtype, const void* out, int total_rows,
                          int num_q_heads, int items, int max_rows, int block_table_width)
 {
@@ -767,14 +767,14 @@ static int ragged_checks(pkv_pool_t pool, int layer, const void* q, int q_dtype,
     const int G = num_q_heads / d.num_kv_heads;
     if (q_dtype != PKV_F16 && q_dtype != PKV_BF16) return PKV_ERR_DTYPE;
     if (!is_quantized(d.kv_dtype) && q_dtype != d.kv_dtype) return PKV_ERR_DTYPE;
-    // grid limits: items in z, (KV head, 16 rows) in y, merge CTAs in x
-    if (items > 65535 || (long long)block_table_width * PKV_BLOCK_SIZE > 0x7fffffffLL ||
-        (long long)d.num_kv_heads * (((long long)max_rows * G + 15) / 16) > 65535 ||
-        (long long)total_rows * num_q_heads > 0x7fffffffLL)
+    // grid limits: items in z, KV heads (up to twice) in y, row tiles and merge CTAs in x; 32-bit rows and keys
+    if (items > 65535 || (long long)block_table_width * PKV_BLOCK_SIZE > 0x7fffffffLL || d.num_kv_heads > 32767 ||
+        (long long)max_rows * G > 0x7fffffffLL - 256 || (long long)total_rows * num_q_heads > 0x7fffffffLL)
         return PKV_ERR_UNSUPPORTED;
     if (items > 0 && max_rows > 0 && total_rows > 0) {
         if (!q || !out) return PKV_ERR_NULL;
-        if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) return PKV_ERR_ARG;
+        // other CTAs may still read q when one writes its rows
+        if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) || q == out) return PKV_ERR_ARG;
     }
     return PKV_OK;
 }

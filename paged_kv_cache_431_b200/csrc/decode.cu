@@ -53,14 +53,15 @@ struct Mma16Cfg {
 // NW = 1: one warp per (partition, KV head or group of 16 of its query heads, sequence).
 // NW > 1 (groups of 17..64 query heads): NW warps share one K/V ring, warp w taking query
 // heads 16w .. 16w+15 of the group, so every K/V tile crosses into the SM once; a stage is
-// refilled once all warps have released it.  RAG: the ragged form, where the rows of a group of
-// 16 are (query row, head) pairs of one item and the output is 16-bit.
+// refilled once all warps have released it.  RAG: the ragged form (NW = 1), where the up to 16
+// rows are (query row, head) pairs of one item and the output is 16-bit.
 template <int D, bool BF16, int NHT, int STAGES, int NW, bool RAG>
 __global__ void __launch_bounds__(32 * NW)
 decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV)
 {
     using Cfg = Mma16Cfg<D, STAGES, NW>;
+    static_assert(!RAG || NW == 1, "the ragged form has one warp");
     extern __shared__ uint8_t smem_dyn[];
     __shared__ __align__(8) uint64_t bars[STAGES];
     __shared__ __align__(8) uint64_t empty[STAGES];
@@ -80,12 +81,12 @@ decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
         if (ragged_beside(p.rg)) return;
         it = ragged_item(p.rg, p.ctx_lens, p.W, p.max_parts * p.part_tokens, b, p.status,
                          threadIdx.x == 0 && part == 0 && blockIdx.y == 0);
-        GC = min(16, it.rows * p.G - 16 * hg);   // query rows of this warp; none: it only helps
+        GC = min(16, it.rows * p.G - 16 * hg);   // query rows of this warp
         ctx = it.end;
         nparts = (ctx - it.base + p.part_tokens - 1) / p.part_tokens;
         tok0 = it.base + part * p.part_tokens;
         lo = 0;
-        if (it.rows * p.G <= (NW > 1 ? 0 : 16 * hg)) return;
+        if (GC <= 0) return;
         if (tok0 >= ctx) {
             if (part == 0 && it.whole) {   // no keys at all: zero rows
                 for (int i = lane; i < GC * (D / 4); i += 32)
@@ -667,7 +668,7 @@ int launch_k(K kernel, int smem, dim3 grid, int threads, cudaStream_t s, const D
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
-template <int D, bool BF16, int NW, bool RAG>
+template <int D, bool BF16, int NW, bool RAG = false>
 int launch_mma16_nw(const DecodeParams& p, int nht, dim3 grid, cudaStream_t s, const CUtensorMap* tmk,
                     const CUtensorMap* tmv)
 {
@@ -679,16 +680,16 @@ int launch_mma16_nw(const DecodeParams& p, int nht, dim3 grid, cudaStream_t s, c
 
 // Groups of 17..64 query heads run as one CTA of ceil(G / 16) warps sharing the K/V ring;
 // wider groups as one single-warp CTA per 16 heads.
-template <int D, bool BF16, bool RAG = false>
+template <int D, bool BF16>
 int launch_mma16(const DecodeParams& p, int nht, dim3 grid, cudaStream_t s, const CUtensorMap* tmk,
                  const CUtensorMap* tmv)
 {
     const dim3 g1(grid.x, grid.y / p.hgroups, grid.z);   // one CTA per KV head
     switch (p.hgroups) {
-    case 2: return launch_mma16_nw<D, BF16, 2, RAG>(p, nht, g1, s, tmk, tmv);
-    case 3: return launch_mma16_nw<D, BF16, 3, RAG>(p, nht, g1, s, tmk, tmv);
-    case 4: return launch_mma16_nw<D, BF16, 4, RAG>(p, nht, g1, s, tmk, tmv);
-    default: return launch_mma16_nw<D, BF16, 1, RAG>(p, nht, grid, s, tmk, tmv);
+    case 2: return launch_mma16_nw<D, BF16, 2>(p, nht, g1, s, tmk, tmv);
+    case 3: return launch_mma16_nw<D, BF16, 3>(p, nht, g1, s, tmk, tmv);
+    case 4: return launch_mma16_nw<D, BF16, 4>(p, nht, g1, s, tmk, tmv);
+    default: return launch_mma16_nw<D, BF16, 1>(p, nht, grid, s, tmk, tmv);
     }
 }
 
@@ -831,10 +832,10 @@ int launch_ragged_short(const RaggedArgs& a, const CUtensorMap* tmk, const CUten
     const int nht = a.max_rows * a.G <= 8 ? 1 : 2;
     if (is_quantized(a.kv_dtype)) return launch_decode_quant_ragged(p, a.kv_dtype, a.d, nht, grid, s, tmk, tmv);
     const bool bf = a.kv_dtype == PKV_BF16;
-    if (a.d == 128) return bf ? launch_mma16<128, true, true>(p, nht, grid, s, tmk, tmv)
-                              : launch_mma16<128, false, true>(p, nht, grid, s, tmk, tmv);
-    return bf ? launch_mma16<64, true, true>(p, nht, grid, s, tmk, tmv)
-              : launch_mma16<64, false, true>(p, nht, grid, s, tmk, tmv);
+    if (a.d == 128) return bf ? launch_mma16_nw<128, true, 1, true>(p, nht, grid, s, tmk, tmv)
+                              : launch_mma16_nw<128, false, 1, true>(p, nht, grid, s, tmk, tmv);
+    return bf ? launch_mma16_nw<64, true, 1, true>(p, nht, grid, s, tmk, tmv)
+              : launch_mma16_nw<64, false, 1, true>(p, nht, grid, s, tmk, tmv);
 }
 
 int launch_ragged_tc(const RaggedArgs& a, bool pair, const CUtensorMap* tmk, const CUtensorMap* tmv, cudaStream_t s)

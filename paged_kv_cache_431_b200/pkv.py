@@ -482,7 +482,7 @@ def paged_cross_attn(pool: KVPool, layer: int, q: torch.Tensor, row_starts: torc
     tp, width = _tables(block_tables, B)
     _check(lib().paged_cross_attn(pool.handle, layer, q.data_ptr(), _dtype_code(q), _int32(row_starts, B + 1, "row_starts"),
                                   rows, H_q, tp, width, _int32(context_lens, B, "context_lens"), B, max_rows,
-                                  max_context_len, scale, out.data_ptr(), wp, wb, _stream_of(stream, idx)),
+                                  max_context_len, float(scale), out.data_ptr(), wp, wb, _stream_of(stream, idx)),
            "paged_cross_attn")
     return out
 
@@ -516,7 +516,7 @@ def paged_decode_attn_groups(pool: KVPool, layer: int, q: torch.Tensor, block_ta
     _check(lib().paged_decode_attn_groups(pool.handle, layer, q.data_ptr(), _dtype_code(q), tp, width,
                                           _int32(context_lens, B, "context_lens"), B, H_q,
                                           _int32(group_starts, n + 1, "group_starts"), _int32(prefix_lens, n, "prefix_lens"),
-                                          n, max_group_size, max_prefix_len, max_suffix_len, scale, out.data_ptr(), wp,
+                                          n, max_group_size, max_prefix_len, max_suffix_len, float(scale), out.data_ptr(), wp,
                                           wb, _stream_of(stream, idx)), "paged_decode_attn_groups")
     return out
 

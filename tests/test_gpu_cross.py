@@ -98,6 +98,36 @@ def test_cross_small_and_large_scales(dt, spread):
         check(out, ref, tolerance(opool, q, ref, [400, 260], scale, True))
 
 
+@pytest.mark.parametrize("dt", [pkv.BF16, pkv.FP8E4M3], ids=lambda x: NAMES[x])
+@pytest.mark.parametrize("scale", [-0.07, 0.0])
+def test_cross_negative_and_zero_scale(dt, scale):
+    for rows in ([2, 1], [130, 50]):
+        pool, opool, q, qd, tables = case(dt, 128, 8, 2, rows, [300, 77], 4850 + dt)
+        out = pkv.paged_cross_attn(pool, 0, q.to(DEV), starts_of(rows).to(DEV), tables.to(DEV),
+                                   torch.tensor([300, 77], dtype=torch.int32, device=DEV), scale, max(rows), 300)
+        ref = reference(opool, q, qd, tables, [300, 77], [0] * rows[0] + [1] * rows[1], scale)
+        check(out, ref, tolerance(opool, q, ref, [300, 77], scale, True))
+
+
+def test_cross_rows_of_very_different_size():
+    """Neighbouring query rows 2^24 apart in size: each keeps its own precision."""
+    for dt in (pkv.BF16, pkv.INT8, pkv.FP8E4M3):
+        for rows in ([4], [40], [150]):
+            pool, opool, q, qd, tables = case(dt, 128, 4, 1, rows, [200], 4870 + dt)
+            q[::2] *= 2.0 ** -24
+            out = pkv.paged_cross_attn(pool, 0, q.to(DEV), starts_of(rows).to(DEV), tables.to(DEV),
+                                       torch.tensor([200], dtype=torch.int32, device=DEV), 0.1, rows[0], 200)
+            ref = reference(opool, q, qd, tables, [200], [0] * rows[0], 0.1)
+            check(out, ref, tolerance(opool, q, ref, [200], 0.1, True))
+
+
+@pytest.mark.parametrize("dt", [pkv.BF16, pkv.INT4], ids=lambda x: NAMES[x])
+def test_cross_one_sequence_with_many_rows(dt):
+    """One sequence with thousands of rows against a short state; a batch of many tiny sequences."""
+    run(dt, 64, 2, 2, [3000], [20], 4880 + dt)
+    run(dt, 64, 4, 2, [1] * 700, [1 + i % 40 for i in range(700)], 4890 + dt)
+
+
 def test_cross_bounds_larger_than_needed_and_layers():
     """Host bounds may exceed the real lengths; the layer argument picks the layer."""
     g = wl.generator(4900)
@@ -109,7 +139,7 @@ def test_cross_bounds_larger_than_needed_and_layers():
     q = wl.normal((63, 8, 128), torch.bfloat16, g)
     ref = reference(opool, q, pkv.BF16, tables, ctx, [0] * 3 + [1] * 60, 0.1)
     tol = tolerance(opool, q, ref, ctx, 0.1, True)
-    for mr, mc in ((60, 300), (500, 5000), (61, 301)):
+    for mr, mc in ((60, 300), (500, 5000), (61, 301), (200000, 300)):
         tb = torch.cat([tables, torch.full((2, 400), -1, dtype=torch.int32)], 1).contiguous()
         out = pkv.paged_cross_attn(both, 1, q.to(DEV), starts_of(rows).to(DEV), tb.to(DEV),
                                    torch.tensor(ctx, dtype=torch.int32, device=DEV), 0.1, mr, mc)
