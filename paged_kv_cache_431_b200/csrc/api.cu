@@ -685,7 +685,7 @@ struct RaggedSplit {
 constexpr int kShortRows16 = 16;
 constexpr int kShortRowsQuant = 32;
 constexpr int kRaggedSlots = 12, kShortFixed = 24;
-constexpr int kTcFixed = 5;
+constexpr int kTcFixed = 4, kTcSplit = 3;
 
 // sms: SMs that the launch may count on.
 static RaggedSplit ragged_split(pkv_pool_t pool, int items, int max_rows, int G, int max_tokens, int sms = num_sms())
@@ -698,7 +698,7 @@ static RaggedSplit ragged_split(pkv_pool_t pool, int items, int max_rows, int G,
     // small quantized launches of 17 .. 32 rows: latency counts (32 rows against 2,000 int8 tokens: 25
     // against 20 us)
     if (quant && R > 16 && (long long)items * H_kv * (((long long)max_tokens + 127) / 128) <= 4LL * num_sms()) r.tc = true;
-    r.pair = r.tc && R <= 128;
+    r.pair = false;
     if (!r.tc) {
         // From ~256 (192) KiB of K + V per partition, as in the plain decode, halved down to 128 (192)
         // tokens: the size that makes rounds x (16-token tiles + fixed) smallest, with about
@@ -718,20 +718,25 @@ static RaggedSplit ragged_split(pkv_pool_t pool, int items, int max_rows, int G,
             if (cost(half) < cost(P)) P = half;
         r.part = P;
     } else {
-        // One CTA per SM and a fixed cost per CTA (its query tiles, TMEM, partials: about kTcFixed key
-        // tiles): the split of the keys, in whole 128-key tiles, that makes waves x (tiles + fixed)
-        // smallest.  Filling one wave instead of two took 128 rows against 4 x 32,768 keys from 117 to
-        // 103 us, 512 rows against 8,192 from 161 to 126.
-        const long long ctas = (long long)items * H_kv * ((R + (r.pair ? 127 : 255)) / (r.pair ? 128 : 256));
-        const int tiles = (int)(((long long)max_tokens + 127) / 128), per = r.pair ? 2 : 1;
+        // One CTA per SM and a fixed cost per CTA (kTcFixed key tiles for its query tiles, TMEM and rows,
+        // kTcSplit more where it writes partials to be merged): the form and the split of the keys, in
+        // whole 128-key tiles, that make waves x (tiles + fixed) smallest.  Filling one wave instead of
+        // two took 128 rows against 4 x 32,768 keys from 117 to 103 us, 512 rows against 8,192 from 161
+        // to 126; up to 128 rows against short keys are not worth two partitions per CTA (64 x 16 heads,
+        // 256 keys: 128 us as pairs, 58 without).
+        const int tiles = (int)(((long long)max_tokens + 127) / 128);
         long long best = -1;
-        int parts = per;
-        for (int k = 1; k <= 64 && (k == 1 || (k * per * 2 <= tiles && (long long)items * k <= 65535)); ++k) {
-            const long long waves = (ctas * k + sms - 1) / sms;
-            const long long cost = waves * ((tiles + k * per - 1) / (k * per) + kTcFixed);
-            if (best < 0 || cost < best) {
-                best = cost;
-                parts = k * per;
+        int parts = 1;
+        for (int per = 1; per <= (R <= 128 ? 2 : 1); ++per) {
+            const long long ctas = (long long)items * H_kv * (per == 2 ? 1 : (R + 255) / 256);
+            for (int k = 1; k <= 64 && (k == 1 || (k * per * 2 <= tiles && (long long)items * k <= 65535)); ++k) {
+                const long long waves = (ctas * k + sms - 1) / sms;
+                const long long cost = waves * ((tiles + k * per - 1) / (k * per) + kTcFixed + (k * per > 1 ? kTcSplit : 0));
+                if (best < 0 || cost < best) {
+                    best = cost;
+                    parts = k * per;
+                    r.pair = per == 2;
+                }
             }
         }
         r.part = (tiles + parts - 1) / parts * 128;

@@ -89,6 +89,7 @@ struct Bars {
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];    // 16-bit tiles, ready for the MMAs
     uint64_t ck_full[2], ck_empty[2], cv_full[2], cv_empty[2];   // code tiles
     uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];        // the scales of a key tile
+    uint64_t q_full;           // the query tiles are in shared memory
     uint64_t s_full[2];        // S(x, t) is in TMEM, and every earlier MMA of the CTA is done
     uint64_t s_empty[2], pv_done[2];   // P_APART: S(x, t) is in registers; P.V(x, t) is done
     uint64_t p_full[2][2];     // a half of P(x, t) is stored
@@ -270,6 +271,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 mbar_init(smem_u32(&bars.sc_empty[s]), shared ? 8 : 4);
             }
         }
+        mbar_init(smem_u32(&bars.q_full), 8);
         for (int x = 0; x < 2; ++x) {
             mbar_init(smem_u32(&bars.s_full[x]), 1);
             mbar_init(smem_u32(&bars.s_empty[x]), 4);
@@ -298,60 +300,6 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
         }
         return blk;
     };
-    // index of each query row, in rows of D (-1: none), where the first K tile will be
-    int* s_row = reinterpret_cast<int*>(smem + C::QT * TILE);
-    for (int i = threadIdx.x; i < C::QT * kBM; i += C::THREADS)
-        s_row[i] = r0 + i < R ? (int)ragged_row(it, p.G, p.H_q, g, r0 + i) : -1;
-    __syncthreads();                            // s_row, s_vmax and the barriers are initialised
-
-    // ---- Q into shared memory, K-major with the 128-byte swizzle, by plain loads: rows are
-    // gathered (row of the item, head), so any group size packs 128 rows into a tile.  A negative
-    // scale is moved into q, so that the softmax may take maxima before it scales.
-    {
-        constexpr int CH = D / 8;               // 16-byte chunks per row
-        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-        const uint16_t* qh = static_cast<const uint16_t*>(p.q);
-        for (int i = threadIdx.x; i < ((C::QT * kBM * CH + C::THREADS - 1) / C::THREADS) * C::THREADS; i += C::THREADS) {
-            const int row = i / CH, c = i % CH;
-            const int at = row < C::QT * kBM ? s_row[row] : -1;
-            uint4 u = make_uint4(0u, 0u, 0u, 0u);
-            if (at >= 0) u = __ldg(reinterpret_cast<const uint4*>(qh + (size_t)at * D + 8 * c));
-            uint32_t* w = reinterpret_cast<uint32_t*>(&u);
-            if constexpr (C::QUANT) {           // fp16, times a power of two per row (its CH lanes agree on it)
-                float f[8], top = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 v = p.q_bf16 ? unpack2<true>(w[e]) : unpack2<false>(w[e]);
-                    f[2 * e] = v.x;
-                    f[2 * e + 1] = v.y;
-                    top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
-                }
-#pragma unroll
-                for (int o = CH / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const int e = unit_shift(top);
-                const float m = exp2_int(e);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) w[k] = pack2<false>(f[2 * k] * m, f[2 * k + 1] * m);
-                if (row < C::QT * kBM && c == 0) s_rowscale[row] = exp2_int(-e);
-            }
-            if (row < C::QT * kBM) {
-                const int tile = row / kBM, rr = row % kBM;
-                sts128(sQ + tile * TILE + (c >> 3) * (kBM * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), w[0] ^ flip,
-                       w[1] ^ flip, w[2] ^ flip, w[3] ^ flip);
-            }
-        }
-        fence_proxy_async_smem();
-    }
-    // ---- the largest V scale of the CTA's keys: P enters P.V times (V scale / its power of two)
-    if constexpr (C::QUANT) {
-        const int lb0 = key_lo(0) / kBlock, lb1 = (max(key_hi(0), nB > 0 ? key_hi(1) : 0) + kBlock - 1) / kBlock;
-        float m = 0.f;
-        for (int lb = lb0 + threadIdx.x; lb < lb1; lb += C::THREADS)
-            m = fmaxf(m, p.v_scale[(size_t)block_id(lb) * p.H_kv + g]);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0) atomicMax(&s_vmax, __float_as_int(m));     // non-negative: ordered as integers
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -396,17 +344,76 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
         const int lo = key_lo(x), hi = key_hi(x);
         const uint32_t tS = tmem + ((uint32_t)(quarter * 32) << 16) + 256 * x;
         const uint32_t tO = tS + 128, tP = C::P_APART ? tS + 192 : tS;
+        // This warp's 32 query rows into shared memory, K-major with the 128-byte swizzle, by plain loads
+        // (rows are gathered: row of the item, head; any group size packs 128 rows into a tile), several
+        // in flight, while the fetchers already run.  A negative scale is moved into q, so that the
+        // softmax may take maxima before it scales.
+        const int rr = r0 + (PAIR ? 0 : x * kBM) + r;
+        const int at = rr < R ? (int)ragged_row(it, p.G, p.H_q, g, rr) : -1;   // in rows of D
+        if (!PAIR || x == 0) {
+            constexpr int CH = D / 8, RPI = 32 / CH, BATCH = 8;   // 16-byte chunks per row, rows per load
+            const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+            const uint16_t* qh = static_cast<const uint16_t*>(p.q);
+            const int c = lane % CH;
+#pragma unroll 1
+            for (int i0 = 0; i0 < 32 / RPI; i0 += BATCH) {
+                uint4 u[BATCH];
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const int a = __shfl_sync(0xffffffffu, at, (i0 + k) * RPI + lane / CH);
+                    u[k] = a >= 0 ? __ldg(reinterpret_cast<const uint4*>(qh + (size_t)a * D + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const int row = quarter * 32 + (i0 + k) * RPI + lane / CH;
+                    uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+                    if constexpr (C::QUANT) {   // fp16, times a power of two per row (its CH lanes agree on it)
+                        float f[8], top = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 q2 = p.q_bf16 ? unpack2<true>(w[e]) : unpack2<false>(w[e]);
+                            f[2 * e] = q2.x;
+                            f[2 * e + 1] = q2.y;
+                            top = fmaxf(top, fmaxf(fabsf(q2.x), fabsf(q2.y)));
+                        }
+#pragma unroll
+                        for (int o = CH / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const int e = unit_shift(top);
+                        const float m = exp2_int(e);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) w[j] = pack2<false>(f[2 * j] * m, f[2 * j + 1] * m);
+                        if (c == 0) s_rowscale[(PAIR ? 0 : x * kBM) + row] = exp2_int(-e);
+                    }
+                    sts128(sQ + (PAIR ? 0 : x) * TILE + (c >> 3) * (kBM * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                           w[0] ^ flip, w[1] ^ flip, w[2] ^ flip, w[3] ^ flip);
+                }
+            }
+            fence_proxy_async_smem();
+        }
+        // the largest V scale of the CTA's keys: P enters P.V times (V scale / its power of two)
+        if constexpr (C::QUANT) {
+            const int lb0 = key_lo(0) / kBlock, lb1 = (max(key_hi(0), nB > 0 ? key_hi(1) : 0) + kBlock - 1) / kBlock;
+            float m = 0.f;
+            for (int lb = lb0 + (int)threadIdx.x; lb < lb1; lb += 256)
+                m = fmaxf(m, p.v_scale[(size_t)block_id(lb) * p.H_kv + g]);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (lane == 0) atomicMax(&s_vmax, __float_as_int(m));     // non-negative: ordered as integers
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.q_full));
         float sl = fabsf(p.scale_log2);
         float v_unit = 1.f, v_mul = 1.f;
+        bool ok = true;
         if constexpr (C::QUANT) {
+            ok = wait(bars.q_full, 0);
             sl *= s_rowscale[(PAIR ? 0 : x * kBM) + r];
             const int e = unit_shift(__int_as_float(s_vmax));
             v_mul = exp2_int(e);
             v_unit = exp2_int(-e);
         }
         float m_used = -INFINITY, l_run = 0.f;
-        bool ok = true;
-        for (int t = 0; t < nx; ++t) {
+        for (int t = 0; ok && t < nx; ++t) {
             const int n = seq(x, t);
             ok = wait(bars.s_full[x], t & 1);
             if (!ok) break;
@@ -570,10 +577,9 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
         if (ok && nx > 0 &&
             wait(bars.o_done[x], 0)) {
             tc_fence_after();
-            const int rr = r0 + (PAIR ? 0 : x * kBM) + r;
-            const bool valid = rr < R;
+            const bool valid = at >= 0;
             const bool final_out = it.whole && nparts == 1;
-            const size_t row = valid ? ragged_row(it, p.G, p.H_q, g, rr) : 0;
+            const size_t row = valid ? at : 0;
             const size_t slot = ws_slot(p, row, part0 + (PAIR ? x : 0));
             const float inv = (final_out ? (l_run == 0.f ? 0.f : 1.f / l_run) : 1.f) * v_unit;
             if (!final_out && valid)
@@ -699,7 +705,10 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
             umma_commit_w(smem_u32(&bars.s_full[x]));
             umma_commit_w(smem_u32(&bars.k_empty[s]));
         };
-        if (nx > 0) scores(0);
+        if (nx > 0) {
+            ok = wait(bars.q_full, 0);
+            if (ok) scores(0);
+        }
         for (int t = 0; ok && t < nx; ++t) {
             if constexpr (C::P_APART) {
                 if (t + 1 < nx) {

@@ -7,8 +7,8 @@ import pytest
 from paged_kv_cache_431_b200 import pkv
 from tests.test_append_rope_args import pools  # noqa: F401
 
-CROSS = dict(layer=0, q=0x10000, qd=pkv.BF16, starts=0x20000, rows=10, H_q=8, tb=0x30000, W=40, cl=0x40000, B=3, mr=5,
-             mc=600, out=0x50000, ws=None, wsb=0)
+CROSS = dict(layer=0, q=0x10000, qd=pkv.BF16, starts=0x20000, rows=10, H_q=8, tb=0x30000, W=400, cl=0x40000, B=3, mr=5,
+             mc=6000, out=0x50000, ws=None, wsb=0)
 GROUPS = dict(layer=0, q=0x10000, qd=pkv.BF16, tb=0x30000, W=40, cl=0x40000, B=6, H_q=8, starts=0x20000, pl=0x60000, n=2,
               ms=4, mp=320, mx=100, out=0x50000, ws=None, wsb=0)
 
@@ -60,7 +60,7 @@ def test_workspaces(pools):  # noqa: F811
     L = pkv.lib()
     for dt in (pkv.BF16, pkv.INT8):
         p = pools(dt)
-        need = L.paged_cross_workspace_bytes(p, 10, 8, 3, 5, 600)
+        need = L.paged_cross_workspace_bytes(p, 10, 8, 3, 5, 6000)
         assert need > 0 and need % (10 * 8 * (128 + 2) * 4) == 0
         assert L.paged_cross_workspace_bytes(p, 10, 8, 3, 5, 60) == 0       # one partition
         q = dict(qd=pkv.BF16)
