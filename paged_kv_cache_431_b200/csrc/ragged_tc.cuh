@@ -29,8 +29,6 @@
 
 #include <cuda_fp8.h>
 
-#include <type_traits>
-
 #include "decode_common.cuh"
 #include "tcgen05.cuh"
 
@@ -44,6 +42,7 @@ constexpr int kBlocks = kBN / kBlock;            // paged blocks per key tile
 constexpr float kSlack = 8.f;                    // log2 units the running max may lag
 constexpr uint32_t kTmemCols = 512;              // tile x: S and P at 256x, O at 256x + 128
 constexpr int kPolyEvery = 4;                    // of so many pairs of exponentials, one is a polynomial
+constexpr float kTiny = 1.17549435e-38f;
 constexpr int kScaleSlots = 4;                   // key tiles whose scales are kept
 
 template <int D, int DT, bool PAIR>
@@ -412,6 +411,8 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
             v_mul = exp2_int(e);
             v_unit = exp2_int(-e);
         }
+        // a factor of 0 would turn a masked score's -inf into NaN; the smallest normal number serves as well
+        sl = fmaxf(sl, kTiny);
         float m_used = -INFINITY, l_run = 0.f;
         for (int t = 0; ok && t < nx; ++t) {
             const int n = seq(x, t);
@@ -445,7 +446,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
             }
             // the row maximum of the scaled scores, in three-input maxima per paged block
             float mx = -INFINITY;
-#pragma unroll
+#pragma unroll(C::ONE_PASS ? 4 : 1)
             for (int c = 0; c < 4; ++c) {
                 float* w = v[C::ONE_PASS ? c : 0];
                 if constexpr (!C::ONE_PASS) {
@@ -467,12 +468,11 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                     m0 = fmax3(m0, u[10], u[11]);
                     m1 = fmax3(m1, u[12], u[13]);
                     m2[k] = fmaxf(fmax3(m0, u[14], u[15]), m1);
-                    // a block of scale 0 must not turn a masked -inf into NaN: its scores are 0
-                    if constexpr (C::QUANT) m2[k] = m2[k] == -INFINITY ? m2[k] : m2[k] * (sl * sc[2 * c + k].x);
+                    if constexpr (C::QUANT) m2[k] *= fmaxf(sl * sc[2 * c + k].x, kTiny);
                 }
                 mx = fmax3(mx, m2[0], m2[1]);
             }
-            if constexpr (!C::QUANT) mx = mx == -INFINITY ? mx : mx * sl;
+            if constexpr (!C::QUANT) mx *= sl;
             float m_new = m_used;
             if (mx > m_used + kSlack || m_used == -INFINITY) m_new = mx;
             const float alpha = m_used == -INFINITY ? 0.f : ex2(m_used - m_new);
@@ -521,14 +521,19 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
             // P = 2^(factor S - m) in 16 bits, packed into the tile's first 64 columns, in two halves
             const float2 mref2 = make_float2(-mref, -mref);
             float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            auto half_of_p = [&](int half, auto masked) {
-#pragma unroll
+            auto half_of_p = [&](int half) {
+#pragma unroll(C::ONE_PASS ? 2 : 1)
                 for (int cc = 0; cc < 2; ++cc) {
                     const int c = 2 * half + cc;
                     const float* u = v[C::ONE_PASS ? c : 0];
                     if constexpr (!C::ONE_PASS) {
                         tmem_ld32(tS + 32 * c, v[0]);
                         tmem_wait_ld();
+                        if (need_mask) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (32 * c + j >= left) v[0][j] = -INFINITY;
+                        }
                     }
                     uint32_t w[16];
 #pragma unroll
@@ -537,18 +542,14 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                         [[maybe_unused]] float vm = 1.f;
                         if constexpr (C::QUANT) {
                             const float2 kv = sc[2 * c + (e >> 3)];
-                            f = sl * kv.x;
+                            f = fmaxf(sl * kv.x, kTiny);
                             vm = v_mul * kv.y;
                         }
-                        float2 a = ffma2(make_float2(u[2 * e], u[2 * e + 1]), make_float2(f, f), mref2);
-                        if constexpr (decltype(masked)::value) {   // again: -inf times a factor of 0 is NaN
-                            if (32 * c + 2 * e >= left) a.x = -INFINITY;
-                            if (32 * c + 2 * e + 1 >= left) a.y = -INFINITY;
-                        }
+                        const float2 a = ffma2(make_float2(u[2 * e], u[2 * e + 1]), make_float2(f, f), mref2);
                         float2 pp;
-                        // some pairs take the FMA pipe, so that it shares the exponentials with
-                        // the special-function unit (not where -inf may stand)
-                        if (!C::QUANT && !decltype(masked)::value && e % kPolyEvery == kPolyEvery - 1) pp = exp2_poly<C::BF16 ? 3 : 4>(a);
+                        // some pairs take the FMA pipe, so that it shares the exponentials with the
+                        // special-function unit (a masked -inf becomes 2^-126 there, and its V row is 0)
+                        if (!C::QUANT && e % kPolyEvery == kPolyEvery - 1) pp = exp2_poly<C::BF16 ? 3 : 4>(a);
                         else pp = make_float2(ex2(a.x), ex2(a.y));
                         sum2[e & 1] = fadd2(sum2[e & 1], pp);
                         if constexpr (C::QUANT) pp = fmul2(pp, make_float2(vm, vm));
@@ -561,13 +562,8 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[x][half]));
             };
-            if (need_mask) {
-                half_of_p(0, std::true_type{});
-                half_of_p(1, std::true_type{});
-            } else {
-                half_of_p(0, std::false_type{});
-                half_of_p(1, std::false_type{});
-            }
+#pragma unroll(C::ONE_PASS ? 2 : 1)
+            for (int half = 0; half < 2; ++half) half_of_p(half);
             if constexpr (C::QUANT) {
                 if (lane == 0) mbar_arrive(smem_u32(&bars.sc_empty[n % kScaleSlots]));
             }
@@ -758,7 +754,9 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
             const int base = key * C::ROW;
             const int sw = (base >> 7) & C::SWZ;
             const uint32_t row = dst + (key >> 3) * KV<D>::GROUP + (key & 7) * 128;
-#pragma unroll
+            // kept small, like the other loops of this kernel: five kinds of warps share the
+            // instruction cache (fully unrolled, warps waited for instructions more than for MMAs)
+#pragma unroll 2
             for (int c = 0; c < C::ROW / 16; ++c) {
                 uint32_t w[4];
                 lds128(w, code + base + ((c ^ sw) << 4));
