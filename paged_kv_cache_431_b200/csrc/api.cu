@@ -677,13 +677,17 @@ struct RaggedSplit {
 };
 
 // Items of up to this many query rows R per KV head run on the warp-level kernels, above on tcgen05
-// (whose time hardly depends on R up to 128).  Measured, head dim 128, warp-level against tcgen05:
-//   bf16, 64 sequences x 3,000 tokens x 8 KV heads: R 16 130 against 157 us, R 20 168 against 159;
-//   4 x 32,768: R 16 109 against 98, R 32 125 against 101, R 48 174 against 103;
-//   int8, the same: R 16 79-138 against 255, R 20 194 against 260, R 48 282 against 272;
-//   86 against 166, 151 against 168, 204 against 170.
+// (whose time hardly depends on R up to 128).  Measured, head dim 128, warp-level against tcgen05 in us:
+//   64 sequences x 3,000 tokens x 8 KV heads: bf16 R 16 131 : 149, R 20 168 : 153;
+//     int8 R 16 112 : 215, R 20 176 : 218, R 48 282 : 272;  fp8 R 20 206 : 222;  int4 R 20 211 : 224
+//   4 x 32,768 x 8: int8 R 16 79 : 132, R 32 134 : 134;  fp8 R 32 167 : 138;  int4 R 32 152 : 138
 constexpr int kShortRows16 = 16;
-constexpr int kShortRowsQuant = 32;
+constexpr int kShortRowsQuant = 24;
+// 16-bit pools of head dim 128 with few long sequences go to tcgen05 whatever R is: their keys fill one
+// CTA per SM, which reads K/V faster than many one-warp CTAs of few tokens each (R 8 to 16, 8 KV heads:
+// 1 x 32,768 33 against 58 us, 2 x 16,384 32 : 50, 4 x 32,768 88 : 109, 16 x 8,192 87 : 97, 16 x 2,048
+// 31 : 33; 32 x 4,096, two waves, 95 : 95; head dim 64, 4 x 32,768, 63 : 53).
+constexpr int kLongTokens = 2048;
 constexpr int kRaggedSlots = 12, kShortFixed = 24;
 constexpr int kTcFixed = 4, kTcSplit = 3;
 
@@ -695,8 +699,9 @@ static RaggedSplit ragged_split(pkv_pool_t pool, int items, int max_rows, int G,
     const long long R = (long long)max_rows * G;
     const int H_kv = pool->d.num_kv_heads;
     r.tc = R > (quant ? kShortRowsQuant : kShortRows16);
-    // small quantized launches of 17 .. 32 rows: latency counts (32 rows against 2,000 int8 tokens: 25
-    // against 20 us)
+    if (!quant && pool->d.head_dim == 128 && max_tokens >= kLongTokens && (long long)items * H_kv <= sms) r.tc = true;
+    // small quantized launches of more than 16 rows: latency counts (32 rows against 2,000 int8 tokens:
+    // 25 against 20 us)
     if (quant && R > 16 && (long long)items * H_kv * (((long long)max_tokens + 127) / 128) <= 4LL * num_sms()) r.tc = true;
     r.pair = false;
     if (!r.tc) {
