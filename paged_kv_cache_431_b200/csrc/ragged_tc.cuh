@@ -61,8 +61,8 @@ struct Cfg {
     static constexpr int CONV = PAIR ? 4 : 2;                     // converter warps for K, and for V (quantized pools)
     static constexpr int THREADS = QUANT ? 384 + 64 * CONV : 384;
     // A softmax thread keeps its row's 128 scores in registers, but for the PAIR form of quantized
-    // pools: there eight converter warps are worth more (fp8, 48 rows against 4 x 32,768 keys: 169 ->
-    // 150 us; with shared tiles, where a tile is converted for 256 rows, 785 -> 813 us).  The block is
+    // pools: there eight converter warps are worth more (fp8, 48 rows against 4 x 32,768 keys: 150 ->
+    // 138 us; with shared tiles, where a tile is converted for 256 rows, 773 -> 808 us).  The block is
     // launched with 168, 128 or 96 a thread, and the softmax warpgroups take what the others release:
     // 2 x 216 + 72 = 3 x 168;  2 x 168 + 72 + 96 <= 4 x 128;  2 x 136 + 56 + 2 x 72 <= 5 x 96.
     static constexpr bool ONE_PASS = !QUANT || !PAIR;
@@ -92,6 +92,7 @@ struct Bars {
     uint64_t s_full[2];        // S(x, t) is in TMEM, and every earlier MMA of the CTA is done
     uint64_t s_empty[2], pv_done[2];   // P_APART: S(x, t) is in registers; P.V(x, t) is done
     uint64_t p_full[2][2];     // a half of P(x, t) is stored
+    uint64_t turn[2];          // P_APART: three quarters of P(x, t) are
     uint64_t o_done[2];
     uint64_t mma_drain[2];
 };
@@ -241,6 +242,10 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
     const int nA = ntiles(0), nB = ntiles(1);
     auto seq = [&](int x, int t) { return shared ? t : x == 0 ? t + min(t, nB) : t + min(t + 1, nA); };
 
+    // Softmax warps of tile x that have rows (32 each).  The others have nothing to compute: what
+    // they would leave in TMEM only reaches rows of O that nobody reads.
+    auto busy = [&](int x) { return min(4, (max(1, R - r0 - (PAIR ? 0 : x * kBM)) + 31) / 32); };
+
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
     const uint32_t sQ = smem_u32(smem);
     const uint32_t sK = sQ + C::QT * TILE;
@@ -267,16 +272,17 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
             }
             for (int s = 0; s < kScaleSlots; ++s) {
                 mbar_init(smem_u32(&bars.sc_full[s]), C::CONV);
-                mbar_init(smem_u32(&bars.sc_empty[s]), shared ? 8 : 4);
+                mbar_init(smem_u32(&bars.sc_empty[s]), shared ? busy(0) + busy(1) : busy(0));
             }
         }
         mbar_init(smem_u32(&bars.q_full), 8);
         for (int x = 0; x < 2; ++x) {
             mbar_init(smem_u32(&bars.s_full[x]), 1);
-            mbar_init(smem_u32(&bars.s_empty[x]), 4);
+            mbar_init(smem_u32(&bars.s_empty[x]), busy(x));
             mbar_init(smem_u32(&bars.pv_done[x]), 1);
-            mbar_init(smem_u32(&bars.p_full[x][0]), 4);
-            mbar_init(smem_u32(&bars.p_full[x][1]), 4);
+            mbar_init(smem_u32(&bars.p_full[x][0]), busy(x));
+            mbar_init(smem_u32(&bars.p_full[x][1]), busy(x));
+            mbar_init(smem_u32(&bars.turn[x]), busy(x));
             mbar_init(smem_u32(&bars.o_done[x]), 1);
         }
         for (int x = 0; x < 2; ++x) mbar_init(smem_u32(&bars.mma_drain[x]), 1);
@@ -339,7 +345,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
         const int x = warp >> 2;
         const int quarter = warp & 3;                             // the 32 TMEM lanes this warp may touch
         const int r = quarter * 32 + lane;
-        const int nx = x == 0 ? nA : nB;
+        const int nx = quarter >= busy(x) ? 0 : x == 0 ? nA : nB;
         const int lo = key_lo(x), hi = key_hi(x);
         const uint32_t tS = tmem + ((uint32_t)(quarter * 32) << 16) + 256 * x;
         const uint32_t tO = tS + 128, tP = C::P_APART ? tS + 192 : tS;
@@ -444,6 +450,11 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                         if (j >= left) v[j >> 5][j & 31] = -INFINITY;
                 }
             }
+            // P_APART: whether P.V(t-1) is done, asked here so that the answer comes beside the maxima
+            bool pv_there = true;
+            if constexpr (C::P_APART) {
+                if (t > 0) pv_there = mbar_test_wait(smem_u32(&bars.pv_done[x]), (t - 1) & 1);
+            }
             // the row maximum of the scaled scores, in three-input maxima per paged block
             float mx = -INFINITY;
 #pragma unroll(C::ONE_PASS ? 4 : 1)
@@ -479,7 +490,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
             const float mref = m_new == -INFINITY ? 0.f : m_new;
             // the max moved: rescale this row of O (P.V(t-1) is done: s_full(t) says so, or pv_done)
             if constexpr (C::P_APART) {
-                if (t > 0) ok = wait(bars.pv_done[x], (t - 1) & 1);
+                if (!__all_sync(0xffffffffu, pv_there)) ok = wait(bars.pv_done[x], (t - 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -502,7 +513,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 if (!ok) break;
                 const int tid = threadIdx.x & 127;
                 const int rows = kBN - left;
-                for (int i = tid; i < C::HALVES * rows * 8; i += 128) {
+                for (int i = tid; i < C::HALVES * rows * 8; i += 32 * busy(x)) {
                     const int c16 = i & 7, row = left + (i >> 3) % rows, half = (i >> 3) / rows;
                     sts128(sV + s * TILE + (row >> 3) * KV<D>::GROUP + half * KV<D>::HALF + (row & 7) * 128 + c16 * 16, 0u,
                            0u, 0u, 0u);
@@ -511,11 +522,14 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 __syncwarp();
             }
             // A and B take turns with the exponentials: left alone they fall into step, and then wait
-            // for the tensor cores together (617 -> 500 us on 1,024 rows x 8 heads against 4 x 4,096
-            // keys).  Quantized pools are bound by the conversions and run faster without it.
+            // for the tensor cores together (head dim 128, 1,024 rows x 8 heads against 4 x 4,096 keys:
+            // 598 us without turns, 460 with).  Head dim 64 is bound by the exponentials themselves and
+            // their waits, so its turn passes after three quarters (394 -> 372 us; 128: 460 -> 469).
+            // Quantized pools are bound by the conversions and run faster without turns.
             if (!C::QUANT && shared) {
-                if (x == 1) ok = wait(bars.p_full[0][1], t & 1);
-                else if (t > 0) ok = wait(bars.p_full[1][1], (t - 1) & 1);
+                uint64_t& turn = C::P_APART ? bars.turn[1 - x] : bars.p_full[1 - x][1];
+                if (x == 1) ok = wait(turn, t & 1);
+                else if (t > 0) ok = wait(turn, (t - 1) & 1);
                 if (!ok) break;
             }
             // P = 2^(factor S - m) in 16 bits, packed into the tile's first 64 columns, in two halves
@@ -556,6 +570,10 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                         w[e] = pack2<C::BF16>(pp.x, pp.y);
                     }
                     tmem_st16u(tP + 16 * c, w);
+                    if (C::P_APART && c == 2) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&bars.turn[x]));
+                    }
                 }
                 tmem_wait_st();
                 tc_fence_before();
