@@ -2,6 +2,7 @@
 // workspace layout and kernel launches.  Every entry point validates on the host
 // before launching and returns a PKV_* status; nothing here synchronizes except
 // pkv_read_device_status.
+#include <algorithm>
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -677,10 +678,14 @@ struct RaggedSplit {
 };
 
 // Items of up to this many query rows R per KV head run on the warp-level kernels, above on tcgen05
-// (whose time hardly depends on R up to 128).  Measured, head dim 128, warp-level against tcgen05 in us:
+// (whose time grows slowly with R up to 128).  Measured, head dim 128, warp-level against tcgen05 in us:
 //   64 sequences x 3,000 tokens x 8 KV heads: bf16 R 16 131 : 149, R 20 168 : 153;
-//     int8 R 16 112 : 215, R 20 176 : 218, R 48 282 : 272;  fp8 R 20 206 : 222;  int4 R 20 211 : 224
-//   4 x 32,768 x 8: int8 R 16 79 : 132, R 32 134 : 134;  fp8 R 32 167 : 138;  int4 R 32 152 : 138
+//     int8 R 16 112 : 170, R 24 176 : 175;  fp8 R 16 130 : 187, R 24 205 : 192;  int4 121 : 179, 212 : 184
+//   4 x 32,768 x 8: int8 R 16 79 : 97, R 24 134 : 98;  fp8 98 : 110, 158 : 112;  int4 89 : 103, 147 : 103
+// The warp-level kernels take 16 rows at a time, so on quantized pools R of 17 to 24 counts only if the
+// rows' mean is above 16 too (64 sequences of 1 to 5 rows of 4 heads, int8: 159 : 202) or where latency
+// counts (32 x 2,000 tokens, int8: 25 : 20); R of 9 to 16 goes to tcgen05 for few long sequences
+// (1 x 4,096, 8 KV heads, int8 23 : 17, fp8 23 : 18; 1 x 32,768 49 : 40, 54 : 42; 2 x 16,384 40 : 39).
 constexpr int kShortRows16 = 16;
 constexpr int kShortRowsQuant = 24;
 // 16-bit pools of head dim 128 with few long sequences go to tcgen05 whatever R is: their keys fill one
@@ -692,17 +697,20 @@ constexpr int kRaggedSlots = 12, kShortFixed = 24;
 constexpr int kTcFixed = 4, kTcSplit = 3;
 
 // sms: SMs that the launch may count on.
-static RaggedSplit ragged_split(pkv_pool_t pool, int items, int max_rows, int G, int max_tokens, int sms = num_sms())
+static RaggedSplit ragged_split(pkv_pool_t pool, int items, int max_rows, double rows, int G, int max_tokens,
+                                int sms = num_sms())
 {
     RaggedSplit r;
     const bool quant = is_quantized(pool->d.kv_dtype);
     const long long R = (long long)max_rows * G;
     const int H_kv = pool->d.num_kv_heads;
-    r.tc = R > (quant ? kShortRowsQuant : kShortRows16);
-    if (!quant && pool->d.head_dim == 128 && max_tokens >= kLongTokens && (long long)items * H_kv <= sms) r.tc = true;
-    // small quantized launches of more than 16 rows: latency counts (32 rows against 2,000 int8 tokens:
-    // 25 against 20 us)
-    if (quant && R > 16 && (long long)items * H_kv * (((long long)max_tokens + 127) / 128) <= 4LL * num_sms()) r.tc = true;
+    if (quant) {
+        r.tc = R > kShortRowsQuant || rows * G > 16 ||
+               (R > 16 && (long long)items * H_kv * (((long long)max_tokens + 127) / 128) <= 4LL * num_sms()) ||
+               (R > 8 && max_tokens >= kLongTokens && 8LL * items * H_kv <= sms);
+    } else {
+        r.tc = R > kShortRows16 || (pool->d.head_dim == 128 && max_tokens >= kLongTokens && (long long)items * H_kv <= sms);
+    }
     r.pair = false;
     if (!r.tc) {
         // From ~256 (192) KiB of K + V per partition, as in the plain decode, halved down to 128 (192)
@@ -822,8 +830,12 @@ size_t paged_cross_workspace_bytes(pkv_pool_t pool, int total_rows, int num_q_he
     if (!pool || total_rows < 0 || num_q_heads <= 0 || num_q_heads % pool->d.num_kv_heads || num_seqs < 0 ||
         max_rows < 0 || max_context_len < 0)
         return 0;
-    const RaggedSplit sp = ragged_split(pool, num_seqs, max_rows, num_q_heads / pool->d.num_kv_heads, max_context_len);
-    return sp.parts > 1 ? ragged_ws_bytes(pool, total_rows, num_q_heads, sp.parts) : 0;
+    // the kernel goes by the rows' mean too: enough for this call and for one of fewer rows
+    const int G = num_q_heads / pool->d.num_kv_heads;
+    const double mean = num_seqs > 0 ? (double)total_rows / num_seqs : 0.;
+    const int parts = std::max(ragged_split(pool, num_seqs, max_rows, mean, G, max_context_len).parts,
+                               ragged_split(pool, num_seqs, max_rows, 0., G, max_context_len).parts);
+    return parts > 1 ? ragged_ws_bytes(pool, total_rows, num_q_heads, parts) : 0;
 }
 
 int paged_cross_attn(pkv_pool_t pool, int layer, const void* q, int q_dtype, const int32_t* row_starts, int total_rows,
@@ -839,7 +851,7 @@ int paged_cross_attn(pkv_pool_t pool, int layer, const void* q, int q_dtype, con
     if (!row_starts || !block_tables || !context_lens) return PKV_ERR_NULL;
     RaggedArgs a = ragged_args(pool, layer, q, q_dtype, num_q_heads, scale, total_rows, block_tables,
                                block_table_width, context_lens, row_starts, out);
-    const RaggedSplit sp = ragged_split(pool, num_seqs, max_rows, a.G, max_context_len);
+    const RaggedSplit sp = ragged_split(pool, num_seqs, max_rows, (double)total_rows / num_seqs, a.G, max_context_len);
     const size_t need = sp.parts > 1 ? ragged_ws_bytes(pool, total_rows, num_q_heads, sp.parts) : 0;
     if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15)))
         return PKV_ERR_WORKSPACE;
@@ -867,7 +879,7 @@ static RaggedSplit prefix_split(pkv_pool_t pool, int num_groups, int max_group_s
     const double tiles = (double)num_groups * d.num_kv_heads * ((rows + 255) / 256) * ((max_prefix_len + 127) / 128);
     const double prefix_us = tiles * 2.2 / num_sms();
     const double suffix_us = (double)num_seqs * max_suffix_len * d.num_kv_heads * 2 * pool->row_bytes / 6.5e6;
-    return ragged_split(pool, num_groups, max_group_size, G, max_prefix_len,
+    return ragged_split(pool, num_groups, max_group_size, (double)num_seqs / num_groups, G, max_prefix_len,
                         suffix_us > prefix_us ? (num_sms() + 1) / 2 : num_sms());
 }
 
@@ -880,7 +892,7 @@ size_t paged_decode_groups_workspace_bytes(pkv_pool_t pool, int num_seqs, int nu
     const int G = num_q_heads / pool->d.num_kv_heads;
     const int pre = max_prefix_len > 0 ? prefix_split(pool, num_groups, max_group_size, G, max_prefix_len, num_seqs,
                                                       max_suffix_len).parts : 0;
-    const int own = ragged_split(pool, num_seqs, 1, G, max_suffix_len).parts;
+    const int own = ragged_split(pool, num_seqs, 1, 1., G, max_suffix_len).parts;
     return pre + own > 1 ? ragged_ws_bytes(pool, num_seqs, num_q_heads, pre + own) : 0;
 }
 
@@ -904,7 +916,7 @@ int paged_decode_attn_groups(pkv_pool_t pool, int layer, const void* q, int q_dt
     const RaggedSplit pre = max_prefix_len > 0 ? prefix_split(pool, num_groups, max_group_size, a.G, max_prefix_len,
                                                               num_seqs, max_suffix_len)
                                                : RaggedSplit{false, false, PKV_BLOCK_SIZE, 0};
-    const RaggedSplit own = ragged_split(pool, num_seqs, 1, a.G, max_suffix_len);
+    const RaggedSplit own = ragged_split(pool, num_seqs, 1, 1., a.G, max_suffix_len);
     const int slots = pre.parts + own.parts;
     const size_t need = slots > 1 ? ragged_ws_bytes(pool, num_seqs, num_q_heads, slots) : 0;
     if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15)))

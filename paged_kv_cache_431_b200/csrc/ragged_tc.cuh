@@ -61,7 +61,7 @@ struct Cfg {
     static constexpr int CONV = PAIR ? 4 : 2;                     // converter warps for K, and for V (quantized pools)
     static constexpr int THREADS = QUANT ? 384 + 64 * CONV : 384;
     // A softmax thread keeps its row's 128 scores in registers, but for the PAIR form of quantized
-    // pools: there eight converter warps are worth more (fp8, 48 rows against 4 x 32,768 keys: 150 ->
+    // pools: there eight converter warps are worth more (fp8, 128 rows against 4 x 32,768 keys: 150 ->
     // 138 us; with shared tiles, where a tile is converted for 256 rows, 773 -> 808 us).  The block is
     // launched with 168, 128 or 96 a thread, and the softmax warpgroups take what the others release:
     // 2 x 216 + 72 = 3 x 168;  2 x 168 + 72 + 96 <= 4 x 128;  2 x 136 + 56 + 2 x 72 <= 5 x 96.
@@ -71,6 +71,14 @@ struct Cfg {
     // Head dim 64 leaves 64 columns of TMEM per tile, which hold P apart from S: S(t+1) is computed
     // as soon as S(t) is in registers, beside the exponentials (else only after P(t).V).
     static constexpr bool P_APART = D == 64 && ONE_PASS;
+    // PAIR form of quantized pools: up to 64 (32) query rows are put into the tile two (four) times, and
+    // each copy takes the softmax of its half (quarter) of a tile's keys, with P = 0 for the others, a
+    // running maximum of its own and its own rows of O; the copies are joined at the end.  Else half
+    // (three quarters) of the softmax warps would have no rows, and the rest all the exponentials
+    // (4 x 32,768 int8 tokens, 8 KV heads: 48 rows 132 -> 118 us, 32 rows 132 -> 99).  What is left is
+    // near shared memory's rate: a key tile is written there by the copies, read and written (twice the
+    // bytes) by the converters, and read by the MMAs together with Q.
+    static constexpr bool COPIES = QUANT && PAIR;
     static constexpr int SWZ = ROW >= 128 ? 7 : ROW == 64 ? 3 : 1;   // TMA swizzle of a code tile
     static_assert(SMEM <= 225 * 1024, "dynamic shared memory, with 2 KB left for the static part");
 };
@@ -102,6 +110,11 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b)
     unsigned long long d;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2bits(a)), "l"(f2bits(b)));
     return bitsf2(d);
+}
+
+__device__ __forceinline__ void named_sync(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 template <int N>
@@ -244,7 +257,10 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
 
     // Softmax warps of tile x that have rows (32 each).  The others have nothing to compute: what
     // they would leave in TMEM only reaches rows of O that nobody reads.
-    auto busy = [&](int x) { return min(4, (max(1, R - r0 - (PAIR ? 0 : x * kBM)) + 31) / 32); };
+    const int copies = !C::COPIES ? 1 : R <= 32 ? 4 : R <= 64 ? 2 : 1;
+    auto busy = [&](int x) {
+        return copies > 1 ? 4 : min(4, (max(1, R - r0 - (PAIR ? 0 : x * kBM)) + 31) / 32);
+    };
 
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
     const uint32_t sQ = smem_u32(smem);
@@ -353,7 +369,10 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
         // (rows are gathered: row of the item, head; any group size packs 128 rows into a tile), several
         // in flight, while the fetchers already run.  A negative scale is moved into q, so that the
         // softmax may take maxima before it scales.
-        const int rr = r0 + (PAIR ? 0 : x * kBM) + r;
+        const int rr = C::COPIES ? r & (kBM / copies - 1) : r0 + (PAIR ? 0 : x * kBM) + r;
+        const int copy = C::COPIES ? quarter * copies >> 2 : 0;
+        // this copy's 32-key columns of a tile
+        const int c_lo = C::COPIES ? copy * (4 / copies) : 0, c_hi = C::COPIES ? c_lo + 4 / copies : 4;
         const int at = rr < R ? (int)ragged_row(it, p.G, p.H_q, g, rr) : -1;   // in rows of D
         if (!PAIR || x == 0) {
             constexpr int CH = D / 8, RPI = 32 / CH, BATCH = 8;   // 16-byte chunks per row, rows per load
@@ -458,7 +477,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
             // the row maximum of the scaled scores, in three-input maxima per paged block
             float mx = -INFINITY;
 #pragma unroll(C::ONE_PASS ? 4 : 1)
-            for (int c = 0; c < 4; ++c) {
+            for (int c = c_lo; c < c_hi; ++c) {
                 float* w = v[C::ONE_PASS ? c : 0];
                 if constexpr (!C::ONE_PASS) {
                     tmem_ld32(tS + 32 * c, v[0]);
@@ -535,62 +554,118 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
             // P = 2^(factor S - m) in 16 bits, packed into the tile's first 64 columns, in two halves
             const float2 mref2 = make_float2(-mref, -mref);
             float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            auto half_of_p = [&](int half) {
-#pragma unroll(C::ONE_PASS ? 2 : 1)
-                for (int cc = 0; cc < 2; ++cc) {
-                    const int c = 2 * half + cc;
-                    const float* u = v[C::ONE_PASS ? c : 0];
-                    if constexpr (!C::ONE_PASS) {
-                        tmem_ld32(tS + 32 * c, v[0]);
-                        tmem_wait_ld();
-                        if (need_mask) {
+            auto columns_of_p = [&](int c) {
+                const float* u = v[C::ONE_PASS ? c : 0];
+                if constexpr (!C::ONE_PASS) {
+                    tmem_ld32(tS + 32 * c, v[0]);
+                    tmem_wait_ld();
+                    if (need_mask) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (32 * c + j >= left) v[0][j] = -INFINITY;
-                        }
-                    }
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float f = sl;
-                        [[maybe_unused]] float vm = 1.f;
-                        if constexpr (C::QUANT) {
-                            const float2 kv = sc[2 * c + (e >> 3)];
-                            f = fmaxf(sl * kv.x, kTiny);
-                            vm = v_mul * kv.y;
-                        }
-                        const float2 a = ffma2(make_float2(u[2 * e], u[2 * e + 1]), make_float2(f, f), mref2);
-                        float2 pp;
-                        // some pairs take the FMA pipe, so that it shares the exponentials with the
-                        // special-function unit (a masked -inf becomes 2^-126 there, and its V row is 0)
-                        if (!C::QUANT && e % kPolyEvery == kPolyEvery - 1) pp = exp2_poly<C::BF16 ? 3 : 4>(a);
-                        else pp = make_float2(ex2(a.x), ex2(a.y));
-                        sum2[e & 1] = fadd2(sum2[e & 1], pp);
-                        if constexpr (C::QUANT) pp = fmul2(pp, make_float2(vm, vm));
-                        w[e] = pack2<C::BF16>(pp.x, pp.y);
-                    }
-                    tmem_st16u(tP + 16 * c, w);
-                    if (C::P_APART && c == 2) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&bars.turn[x]));
+                        for (int j = 0; j < 32; ++j)
+                            if (32 * c + j >= left) v[0][j] = -INFINITY;
                     }
                 }
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float f = sl;
+                    [[maybe_unused]] float vm = 1.f;
+                    if constexpr (C::QUANT) {
+                        const float2 kv = sc[2 * c + (e >> 3)];
+                        f = fmaxf(sl * kv.x, kTiny);
+                        vm = v_mul * kv.y;
+                    }
+                    const float2 a = ffma2(make_float2(u[2 * e], u[2 * e + 1]), make_float2(f, f), mref2);
+                    float2 pp;
+                    // some pairs take the FMA pipe, so that it shares the exponentials with the
+                    // special-function unit (a masked -inf becomes 2^-126 there, and its V row is 0)
+                    if (!C::QUANT && e % kPolyEvery == kPolyEvery - 1) pp = exp2_poly<C::BF16 ? 3 : 4>(a);
+                    else pp = make_float2(ex2(a.x), ex2(a.y));
+                    sum2[e & 1] = fadd2(sum2[e & 1], pp);
+                    if constexpr (C::QUANT) pp = fmul2(pp, make_float2(vm, vm));
+                    w[e] = pack2<C::BF16>(pp.x, pp.y);
+                }
+                tmem_st16u(tP + 16 * c, w);
+                if (C::P_APART && c == 2) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bars.turn[x]));
+                }
+            };
+            auto half_done = [&](int half) {
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[x][half]));
             };
+            if constexpr (C::COPIES) {
+#pragma unroll 1
+                for (int c = c_lo; c < c_hi; ++c) {
+                    columns_of_p(c);
+                    if (copies == 1 && c == 1) half_done(0);
+                }
+                if (copies > 1) {                                 // the other copies' keys
+                    const uint32_t none[16] = {};
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c)
+                        if (c < c_lo || c >= c_hi) tmem_st16u(tP + 16 * c, none);
+                    half_done(0);
+                }
+                half_done(1);
+            } else {
 #pragma unroll(C::ONE_PASS ? 2 : 1)
-            for (int half = 0; half < 2; ++half) half_of_p(half);
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll(C::ONE_PASS ? 2 : 1)
+                    for (int cc = 0; cc < 2; ++cc) columns_of_p(2 * half + cc);
+                    half_done(half);
+                }
+            }
             if constexpr (C::QUANT) {
                 if (lane == 0) mbar_arrive(smem_u32(&bars.sc_empty[n % kScaleSlots]));
             }
             l_run = l_run * alpha + ((sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y));
             m_used = m_new;
         }
-        if (ok && nx > 0 &&
-            wait(bars.o_done[x], 0)) {
-            tc_fence_after();
+        bool done = ok && nx > 0 && wait(bars.o_done[x], 0);
+        if (done) tc_fence_after();
+        // Join the copies: their O, brought to the common maximum, through the rings, which nothing
+        // uses any more once the MMAs of both tiles are done.  Every softmax warp comes here, on an
+        // abort too (the rings may then still be written to; what is computed is not used).
+        float factor = 1.f;
+        const float4* others = nullptr;
+        if (C::COPIES && copies > 1) {
+            const int rows = kBM / copies;
+            float2* ml = reinterpret_cast<float2*>(smem) + x * kBM;
+            float4* red = reinterpret_cast<float4*>(smem + TILE + x * NS * TILE);   // [copy - 1][D / 4][rows]
+            named_sync(1, 256);
+            ml[r] = make_float2(m_used, l_run);
+            named_sync(2 + x, 128);
+            float m = -INFINITY, l = 0.f;
+            for (int k = 0; k < copies; ++k) m = fmaxf(m, ml[k * rows + rr].x);
+            for (int k = 0; k < copies; ++k) {
+                const float2 u = ml[k * rows + rr];
+                l += u.x == -INFINITY ? 0.f : ex2(u.x - m) * u.y;
+            }
+            factor = m_used == -INFINITY ? 0.f : ex2(m_used - m);
+            m_used = m;
+            l_run = l;
+            if (copy > 0 && done) {
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    tmem_ld32(tO + 32 * c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        red[((copy - 1) * (D / 4) + 8 * c + i) * rows + rr] = make_float4(
+                            o[4 * i] * factor, o[4 * i + 1] * factor, o[4 * i + 2] * factor, o[4 * i + 3] * factor);
+                    __syncwarp();
+                }
+            }
+            named_sync(2 + x, 128);
+            done = done && copy == 0;
+            others = red + rr;
+        }
+        if (done) {
             const bool valid = at >= 0;
             const bool final_out = it.whole && nparts == 1;
             const size_t row = valid ? at : 0;
@@ -604,6 +679,22 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 float o[32];
                 tmem_ld32(tO + 32 * c, o);
                 tmem_wait_ld();
+                if constexpr (C::COPIES) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] *= factor;
+#pragma unroll 1
+                    for (int k = 1; k < copies; ++k) {
+                        const float4* u = others + ((k - 1) * (D / 4) + 8 * c) * (kBM / copies);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 w = u[i * (kBM / copies)];
+                            o[4 * i] += w.x;
+                            o[4 * i + 1] += w.y;
+                            o[4 * i + 2] += w.z;
+                            o[4 * i + 3] += w.w;
+                        }
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] *= inv;
                 if (!valid) {
@@ -799,10 +890,18 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 }
             }
         };
-        auto scales_of = [&](int x, int t) {                      // K warps, threads 0..7: one block of the tile each
+        // K warps, threads 0..7: the scales of one block of the tile each, in two steps, each a tile ahead
+        // of its use, so that nobody waits for a load (fetched in one step, a table entry's use held the
+        // conversions up for 700 cycles a tile)
+        constexpr int kNone = -0x7fffffff - 1;
+        auto entry_of = [&](int x, int t) -> int {
             const int k = key_lo(x) + t * kBN + id * kBlock;
-            if (is_v || id >= kBlocks || k >= key_hi(x)) return make_float2(0.f, 0.f);
-            const size_t i = (size_t)block_id(k / kBlock) * p.H_kv + g;
+            return is_v || id >= kBlocks || (x == 1 && nB == 0) || k >= key_hi(x) ? kNone : trow[k / kBlock];
+        };
+        auto scales_at = [&](int blk) {
+            if (blk == kNone) return make_float2(0.f, 0.f);
+            if ((unsigned)blk >= (unsigned)p.N) blk = 0;          // its fetcher reports it
+            const size_t i = (size_t)blk * p.H_kv + g;
             return make_float2(p.k_scale[i], p.v_scale[i]);
         };
         uint64_t* cfull = is_v ? bars.cv_full : bars.ck_full;
@@ -812,14 +911,16 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
         const uint32_t from = is_v ? sCV : sCK, to = is_v ? sV : sK;
         bool ok = true;
         const int tmax = max(nA, nB);
-        float2 next[2] = {scales_of(0, 0), nB > 0 ? scales_of(1, 0) : make_float2(0.f, 0.f)};
+        float2 next[2] = {scales_at(entry_of(0, 0)), scales_at(entry_of(1, 0))};
+        int blk[2] = {entry_of(0, 1), entry_of(1, 1)};
         for (int t = 0; ok && t < tmax; ++t) {
             for (int x = 0; ok && x < (shared ? 1 : 2); ++x) {
                 const int nx = x == 0 ? nA : nB;
                 if (t >= nx) continue;
                 const int n = seq(x, t), s = n % NS, cs = n % NC;
                 const float2 mine = next[x];
-                if (t + 1 < nx) next[x] = scales_of(x, t + 1);
+                next[x] = scales_at(blk[x]);
+                blk[x] = entry_of(x, t + 2);
                 const int left = key_hi(x) - key_lo(x) - t * kBN;
                 ok = wait(cfull[cs], (n / NC) & 1) && (n < NS || wait(empty[s], ((n - NS) / NS) & 1));
                 // the softmax warps release a slot of scales

@@ -70,6 +70,21 @@ def test_cross_many_sequences_and_rows(dt):
     run(dt, 128, 8, 2, rows, ctx, 4501 + dt, pad=4)
 
 
+@pytest.mark.parametrize("dt", pkv.QUANTIZED, ids=lambda x: NAMES[x])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [[4, 3, 1, 2, 0, 4], [4, 3, 8, 1, 6, 5], [4, 3, 8, 12, 6, 16]])
+def test_cross_rows_shared_out_over_keys(dt, d, rows):
+    """8 to 128 query rows per KV head in one launch (up to 32, up to 64 and more are treated
+    differently), with last tiles of 1, 40, 72 and 104 keys and partitions of one tile."""
+    run(dt, d, 16, 2, rows, [5000, 129, 2088, 40, 300, 3176], 4600 + dt + d + rows[3], pad=2, gain=4.0)
+
+
+@pytest.mark.parametrize("dt", pkv.QUANTIZED, ids=lambda x: NAMES[x])
+def test_cross_peaked_rows_shared_out_over_keys(dt):
+    """Logits of up to several hundred, so that a row's parts differ by factors beyond 2^126."""
+    run(dt, 128, 8, 1, [4, 2, 6], [1300, 20000, 515], 4650 + dt, gain=60.0)
+
+
 @pytest.mark.parametrize("dt", [pkv.BF16, pkv.F16, pkv.FP8E4M3, pkv.INT8], ids=lambda x: NAMES[x])
 @pytest.mark.parametrize("rows", [1, 130])
 def test_cross_long_state(dt, rows):
