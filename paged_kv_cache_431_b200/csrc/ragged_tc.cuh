@@ -61,8 +61,8 @@ struct Cfg {
     static constexpr int CONV = PAIR ? 4 : 2;                     // converter warps for K, and for V (quantized pools)
     static constexpr int THREADS = QUANT ? 384 + 64 * CONV : 384;
     // A softmax thread keeps its row's 128 scores in registers, but for the PAIR form of quantized
-    // pools: there eight converter warps are worth more (fp8, 128 rows against 4 x 32,768 keys: 150 ->
-    // 138 us; with shared tiles, where a tile is converted for 256 rows, 773 -> 808 us).  The block is
+    // pools: there eight converter warps are worth more (fp8, 48 rows against 4 x 32,768 keys, before
+    // COPIES below: 150 -> 138 us; with shared tiles, converted once for 256 rows, 773 -> 808 us).  The block is
     // launched with 168, 128 or 96 a thread, and the softmax warpgroups take what the others release:
     // 2 x 216 + 72 = 3 x 168;  2 x 168 + 72 + 96 <= 4 x 128;  2 x 136 + 56 + 2 x 72 <= 5 x 96.
     static constexpr bool ONE_PASS = !QUANT || !PAIR;
@@ -75,9 +75,9 @@ struct Cfg {
     // each copy takes the softmax of its half (quarter) of a tile's keys, with P = 0 for the others, a
     // running maximum of its own and its own rows of O; the copies are joined at the end.  Else half
     // (three quarters) of the softmax warps would have no rows, and the rest all the exponentials
-    // (4 x 32,768 int8 tokens, 8 KV heads: 48 rows 132 -> 118 us, 32 rows 132 -> 99).  What is left is
-    // near shared memory's rate: a key tile is written there by the copies, read and written (twice the
-    // bytes) by the converters, and read by the MMAs together with Q.
+    // (4 x 32,768 int8 tokens, 8 KV heads: 48 rows 132 -> 118 us, 32 rows 132 -> 99).  What is left
+    // is a chain: the MMAs of A and of B, 128 rows each whatever R is, one after the other (2,200 cycles
+    // of 4,700 per pair of tiles), and the softmax of each.
     static constexpr bool COPIES = QUANT && PAIR;
     static constexpr int SWZ = ROW >= 128 ? 7 : ROW == 64 ? 3 : 1;   // TMA swizzle of a code tile
     static_assert(SMEM <= 225 * 1024, "dynamic shared memory, with 2 KB left for the static part");
