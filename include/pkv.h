@@ -343,7 +343,8 @@ PKV_API size_t paged_decode_groups_workspace_bytes(pkv_pool_t pool, int num_seqs
  *        padding: their output rows are left as they are.
  *   prefix_lens [device]: int32 [num_groups], multiples of 16; 0: the group shares nothing.
  *   max_group_size, max_prefix_len, max_suffix_len [host]: bounds of a group's sequences, of
- *        prefix_lens, and of context_len - prefix_len; they size the grids.
+ *        prefix_lens, and of context_len - prefix_len (the lengths together at most 2^30); they size
+ *        the grids.
  *   workspace [device]: paged_decode_groups_workspace_bytes(...) bytes, 16-byte aligned.
  * All pool dtypes, head dims and group sizes.  On the device: lengths and group_starts out of
  * range are clipped to the bounds and set PKV_DEV_BAD_LENGTH; a prefix that is no multiple of 16
@@ -375,7 +376,8 @@ PKV_API size_t paged_cross_workspace_bytes(pkv_pool_t pool, int total_rows, int 
  *   row_starts [device]: int32 [num_seqs + 1], ascending, in [0, total_rows].  A sequence may have
  *        no rows; rows of no sequence (behind the last) are padding, their output is left as it is.
  *   block_tables, context_lens [device]: as paged_decode_attn.
- *   max_rows, max_context_len [host]: bounds of a sequence's rows and of context_lens.
+ *   max_rows, max_context_len [host]: bounds of a sequence's rows and of context_lens (the latter
+ *        at most 2^30).
  *   workspace [device]: paged_cross_workspace_bytes(...) bytes, 16-byte aligned.
  * All pool dtypes, head dims and group sizes.  On the device: lengths and row_starts out of range
  * are clipped to the bounds and set PKV_DEV_BAD_LENGTH (rows past max_rows are not written).

@@ -693,6 +693,9 @@ constexpr int kShortRowsQuant = 24;
 // 1 x 32,768 33 against 58 us, 2 x 16,384 32 : 50, 4 x 32,768 88 : 109, 16 x 8,192 87 : 97, 16 x 2,048
 // 31 : 33; 32 x 4,096, two waves, 95 : 95; head dim 64, 4 x 32,768, 63 : 53).
 constexpr int kLongTokens = 2048;
+// Bounds of lengths above this are refused: the kernels add a partition (at most one length) to a
+// position in 32 bits.
+constexpr int kMaxRaggedTokens = 1 << 30;
 constexpr int kRaggedSlots = 12, kShortFixed = 24;
 constexpr int kTcFixed = 4, kTcSplit = 3;
 
@@ -847,6 +850,7 @@ int paged_cross_attn(pkv_pool_t pool, int layer, const void* q, int q_dtype, con
     int rc = ragged_checks(pool, layer, q, q_dtype, out, total_rows, num_q_heads, num_seqs, max_rows, block_table_width);
     if (rc != PKV_OK) return rc;
     if (max_context_len < 0) return PKV_ERR_ARG;
+    if (max_context_len > kMaxRaggedTokens) return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0 || total_rows == 0 || max_rows == 0) return PKV_OK;
     if (!row_starts || !block_tables || !context_lens) return PKV_ERR_NULL;
     RaggedArgs a = ragged_args(pool, layer, q, q_dtype, num_q_heads, scale, total_rows, block_tables,
@@ -908,6 +912,7 @@ int paged_decode_attn_groups(pkv_pool_t pool, int layer, const void* q, int q_dt
     if (rc != PKV_OK) return rc;
     if (max_prefix_len < 0 || max_suffix_len < 0 || (long long)max_prefix_len + max_suffix_len > 0x7fffffffLL)
         return PKV_ERR_ARG;
+    if ((long long)max_prefix_len + max_suffix_len > kMaxRaggedTokens) return PKV_ERR_UNSUPPORTED;
     if (num_seqs > 65534) return PKV_ERR_UNSUPPORTED;   // grid z: the sequences and one more
     if (num_seqs == 0 || num_groups == 0 || max_group_size == 0) return PKV_OK;
     if (!block_tables || !context_lens || !group_starts || !prefix_lens) return PKV_ERR_NULL;

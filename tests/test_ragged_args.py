@@ -34,14 +34,15 @@ BOTH = [(dict(q=None), -1), (dict(out=None), -1), (dict(starts=None), -1), (dict
 
 @pytest.mark.parametrize("change,status", BOTH + [
     (dict(rows=-1), -2), (dict(mr=-1), -2), (dict(mc=-1), -2), (dict(B=65536), -9), (dict(rows=1 << 28, H_q=8), -9),
-    (dict(mr=1 << 30), -9), (dict(out=0x10000), -2)])
+    (dict(mr=1 << 30), -9), (dict(out=0x10000), -2), (dict(mc=(1 << 30) + 1), -9), (dict(mc=(1 << 31) - 1), -9)])
 def test_cross_refusals(pools, change, status):  # noqa: F811
     assert cross(pools(pkv.BF16), **change) == status
 
 
 @pytest.mark.parametrize("change,status", BOTH + [
     (dict(pl=None), -1), (dict(n=-1), -2), (dict(ms=-1), -2), (dict(mp=-1), -2), (dict(mx=-1), -2),
-    (dict(mp=1 << 30, mx=1 << 30), -2), (dict(n=65536), -9), (dict(B=65535), -9), (dict(out=0x10000), -2)])
+    (dict(mp=1 << 30, mx=1 << 30), -2), (dict(n=65536), -9), (dict(B=65535), -9), (dict(out=0x10000), -2),
+    (dict(mp=1 << 30, mx=1), -9), (dict(mx=(1 << 30) + 1), -9)])
 def test_groups_refusals(pools, change, status):  # noqa: F811
     assert groups(pools(pkv.BF16), **change) == status
 
