@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(32 * kMergeHeads) ragged_merge_kernel(const De
         }
         M = Mn;
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const float inv = 1.f / L;   // L 0: every score -inf, NaN as 0 / 0
     uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(r.out16) + row * D + lane * V);
 #pragma unroll
     for (int e = 0; e < V; e += 2)

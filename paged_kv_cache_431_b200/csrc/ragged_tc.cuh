@@ -129,30 +129,45 @@ __device__ __forceinline__ void regs_dec()
 }
 
 // 2^a for a pair, on the FMA pipe: a = n + f with n the nearest integer (by adding 1.5 x 2^23), 2^f
-// on [-1/2, 1/2] by the minimax polynomial of degree 3 (relative error 2^-13.7, against the half
-// step 2^-9 of a bf16 P) or 4 (2^-18.5, against 2^-12), n added to the exponent field.  a is at most
-// kSlack; below -126 it counts as -126.
+// on [-1/2, 1/2] by the polynomial 1 + f q(f) of least largest relative error, degree 3 (2^-13.2,
+// against the half step 2^-9 of a bf16 P) or 4 (2^-18.4, against 2^-12), n added to the exponent field.
+// a is at most kSlack.  From -127 down the result is exactly 0 (the constant term 1 at n = -127 leaves
+// a field of 0 and no significand), so that a masked score, -inf, weighs nothing; between -127 and -126
+// it is some number below 2^-126.  A NaN comes out as 0: the caller's row sum carries it.
 template <int DEG>
 __device__ __forceinline__ float2 exp2_poly(float2 a)
 {
     constexpr float M = 12582912.f;
-    a = make_float2(fmaxf(a.x, -126.f), fmaxf(a.y, -126.f));
+    a = make_float2(fmaxf(a.x, -127.f), fmaxf(a.y, -127.f));
     const float2 t = fadd2(a, make_float2(M, M));
     const float2 f = fsub2(a, fsub2(t, make_float2(M, M)));
     auto c2 = [](float c) { return make_float2(c, c); };
     float2 y;
     if constexpr (DEG == 3) {
-        y = ffma2(c2(0x1.c3f760p-5f), f, c2(0x1.f0de1ap-3f));
-        y = ffma2(y, f, c2(0x1.62f31ap-1f));
-        y = ffma2(y, f, c2(0x1.fff692p-1f));
+        y = ffma2(c2(0x1.c2a216p-5f), f, c2(0x1.f00c4cp-3f));
+        y = ffma2(y, f, c2(0x1.62f5fap-1f));
     } else {
-        y = ffma2(c2(0x1.3997d6p-7f), f, c2(0x1.ca1440p-5f));
-        y = ffma2(y, f, c2(0x1.ec06dap-3f));
-        y = ffma2(y, f, c2(0x1.62e0dcp-1f));
-        y = ffma2(y, f, c2(0x1.ffffe8p-1f));
+        y = ffma2(c2(0x1.3a02cep-7f), f, c2(0x1.c9fc46p-5f));
+        y = ffma2(y, f, c2(0x1.ec0378p-3f));
+        y = ffma2(y, f, c2(0x1.62e12cp-1f));
     }
+    y = ffma2(y, f, c2(1.f));
     return make_float2(__int_as_float(__float_as_int(y.x) + (__float_as_int(t.x) << 23)),
                        __int_as_float(__float_as_int(y.y) + (__float_as_int(t.y) << 23)));
+}
+
+// Maxima that keep a NaN, so that a row maximum tells whether any of its scores is one.
+__device__ __forceinline__ float fmax_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((127 + e) << 23); }   // e in [-126, 127]
@@ -436,8 +451,9 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
             v_mul = exp2_int(e);
             v_unit = exp2_int(-e);
         }
-        // a factor of 0 would turn a masked score's -inf into NaN; the smallest normal number serves as well
-        sl = fmaxf(sl, kTiny);
+        // a factor of 0 would turn a masked score's -inf into NaN; the smallest normal number serves as
+        // well (a NaN stays: it is the caller's scale)
+        sl = fmax_nan(sl, kTiny);
         float m_used = -INFINITY, l_run = 0.f;
         for (int t = 0; ok && t < nx; ++t) {
             const int n = seq(x, t);
@@ -474,7 +490,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
             if constexpr (C::P_APART) {
                 if (t > 0) pv_there = mbar_test_wait(smem_u32(&bars.pv_done[x]), (t - 1) & 1);
             }
-            // the row maximum of the scaled scores, in three-input maxima per paged block
+            // the row maximum of the scaled scores, in three-input maxima per paged block; NaN if any is
             float mx = -INFINITY;
 #pragma unroll(C::ONE_PASS ? 4 : 1)
             for (int c = c_lo; c < c_hi; ++c) {
@@ -492,17 +508,20 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const float* u = w + 16 * k;
-                    float m0 = fmax3(u[0], u[1], u[2]), m1 = fmax3(u[3], u[4], u[5]);
-                    m0 = fmax3(m0, u[6], u[7]);
-                    m1 = fmax3(m1, u[8], u[9]);
-                    m0 = fmax3(m0, u[10], u[11]);
-                    m1 = fmax3(m1, u[12], u[13]);
-                    m2[k] = fmaxf(fmax3(m0, u[14], u[15]), m1);
-                    if constexpr (C::QUANT) m2[k] *= fmaxf(sl * sc[2 * c + k].x, kTiny);
+                    float m0 = fmax3_nan(u[0], u[1], u[2]), m1 = fmax3_nan(u[3], u[4], u[5]);
+                    m0 = fmax3_nan(m0, u[6], u[7]);
+                    m1 = fmax3_nan(m1, u[8], u[9]);
+                    m0 = fmax3_nan(m0, u[10], u[11]);
+                    m1 = fmax3_nan(m1, u[12], u[13]);
+                    m2[k] = fmax_nan(fmax3_nan(m0, u[14], u[15]), m1);
+                    if constexpr (C::QUANT) m2[k] *= fmax_nan(sl * sc[2 * c + k].x, kTiny);
                 }
-                mx = fmax3(mx, m2[0], m2[1]);
+                mx = fmax3_nan(mx, m2[0], m2[1]);
             }
             if constexpr (!C::QUANT) mx *= sl;
+            // a score of NaN or +inf makes the row's softmax NaN (inf - inf): said once per row and tile,
+            // by its sum, since not every exponential below would (scores of -inf just weigh nothing)
+            const bool undefined = !(mx < INFINITY);
             float m_new = m_used;
             if (mx > m_used + kSlack || m_used == -INFINITY) m_new = mx;
             const float alpha = m_used == -INFINITY ? 0.f : ex2(m_used - m_new);
@@ -578,7 +597,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                     const float2 a = ffma2(make_float2(u[2 * e], u[2 * e + 1]), make_float2(f, f), mref2);
                     float2 pp;
                     // some pairs take the FMA pipe, so that it shares the exponentials with the
-                    // special-function unit (a masked -inf becomes 2^-126 there, and its V row is 0)
+                    // special-function unit
                     if (!C::QUANT && e % kPolyEvery == kPolyEvery - 1) pp = exp2_poly<C::BF16 ? 3 : 4>(a);
                     else pp = make_float2(ex2(a.x), ex2(a.y));
                     sum2[e & 1] = fadd2(sum2[e & 1], pp);
@@ -623,6 +642,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 if (lane == 0) mbar_arrive(smem_u32(&bars.sc_empty[n % kScaleSlots]));
             }
             l_run = l_run * alpha + ((sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y));
+            if (undefined) l_run = NAN;
             m_used = m_new;
         }
         bool done = ok && nx > 0 && wait(bars.o_done[x], 0);
@@ -670,7 +690,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
             const bool final_out = it.whole && nparts == 1;
             const size_t row = valid ? at : 0;
             const size_t slot = ws_slot(p, row, part0 + (PAIR ? x : 0));
-            const float inv = (final_out ? (l_run == 0.f ? 0.f : 1.f / l_run) : 1.f) * v_unit;
+            const float inv = (final_out ? 1.f / l_run : 1.f) * v_unit;   // l_run 0: every score -inf, NaN as 0 / 0
             if (!final_out && valid)
                 st_hint(reinterpret_cast<float2*>(p.ws_ml + slot * 2), make_float2(m_used, l_run), l2_evict_last());
             __syncwarp();
@@ -890,7 +910,8 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 }
             }
         };
-        // K warps, threads 0..7: the scales of one block of the tile each, in two steps, each a tile ahead
+        // K warps, threads 0..7: the scales of one block of the tile each (an infinite K scale counts as
+        // NaN: its code values of 0 have no product), in two steps, each a tile ahead
         // of its use, so that nobody waits for a load (fetched in one step, a table entry's use held the
         // conversions up for 700 cycles a tile)
         constexpr int kNone = -0x7fffffff - 1;
@@ -902,7 +923,8 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
             if (blk == kNone) return make_float2(0.f, 0.f);
             if ((unsigned)blk >= (unsigned)p.N) blk = 0;          // its fetcher reports it
             const size_t i = (size_t)blk * p.H_kv + g;
-            return make_float2(p.k_scale[i], p.v_scale[i]);
+            const float ks = p.k_scale[i];
+            return make_float2(isinf(ks) ? NAN : ks, p.v_scale[i]);
         };
         uint64_t* cfull = is_v ? bars.cv_full : bars.ck_full;
         uint64_t* cempty = is_v ? bars.cv_empty : bars.ck_empty;
