@@ -519,11 +519,8 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 mx = fmax3_nan(mx, m2[0], m2[1]);
             }
             if constexpr (!C::QUANT) mx *= sl;
-            // a score of NaN or +inf makes the row's softmax NaN (inf - inf): said once per row and tile,
-            // by its sum, since not every exponential below would (scores of -inf just weigh nothing)
-            const bool undefined = !(mx < INFINITY);
-            float m_new = m_used;
-            if (mx > m_used + kSlack || m_used == -INFINITY) m_new = mx;
+            // a NaN becomes the row's maximum, and so reaches its sum; one of +inf is looked for behind the loop
+            const float m_new = mx <= m_used + kSlack ? m_used : mx;
             const float alpha = m_used == -INFINITY ? 0.f : ex2(m_used - m_new);
             const float mref = m_new == -INFINITY ? 0.f : m_new;
             // the max moved: rescale this row of O (P.V(t-1) is done: s_full(t) says so, or pv_done)
@@ -642,9 +639,11 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 if (lane == 0) mbar_arrive(smem_u32(&bars.sc_empty[n % kScaleSlots]));
             }
             l_run = l_run * alpha + ((sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y));
-            if (undefined) l_run = NAN;
             m_used = m_new;
         }
+        // a score of +inf makes the row's softmax NaN (inf - inf), which not every exponential above would;
+        // scores of -inf just weigh nothing
+        if (!(m_used < INFINITY)) l_run = NAN;
         bool done = ok && nx > 0 && wait(bars.o_done[x], 0);
         if (done) tc_fence_after();
         // Join the copies: their O, brought to the common maximum, through the rings, which nothing
@@ -910,8 +909,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 }
             }
         };
-        // K warps, threads 0..7: the scales of one block of the tile each (an infinite K scale counts as
-        // NaN: its code values of 0 have no product), in two steps, each a tile ahead
+        // K warps, threads 0..7: the scales of one block of the tile each, in two steps, each a tile ahead
         // of its use, so that nobody waits for a load (fetched in one step, a table entry's use held the
         // conversions up for 700 cycles a tile)
         constexpr int kNone = -0x7fffffff - 1;
@@ -923,8 +921,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
             if (blk == kNone) return make_float2(0.f, 0.f);
             if ((unsigned)blk >= (unsigned)p.N) blk = 0;          // its fetcher reports it
             const size_t i = (size_t)blk * p.H_kv + g;
-            const float ks = p.k_scale[i];
-            return make_float2(isinf(ks) ? NAN : ks, p.v_scale[i]);
+            return make_float2(p.k_scale[i], p.v_scale[i]);
         };
         uint64_t* cfull = is_v ? bars.cv_full : bars.ck_full;
         uint64_t* cempty = is_v ? bars.cv_empty : bars.ck_empty;
@@ -949,7 +946,10 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 if (!is_v && ok && n >= kScaleSlots) ok = wait(bars.sc_empty[n % kScaleSlots], ((n - kScaleSlots) / kScaleSlots) & 1);
                 if (!ok) break;
                 if (id == 0) s_armed[is_v ? 1 : 0] = n + 1;
-                if (!is_v && id < kBlocks) s_scale[(n % kScaleSlots) * kBlocks + id] = mine;
+                // an infinite K scale counts as NaN (its codes of 0 have no product); looked at here, where
+                // the load is back
+                if (!is_v && id < kBlocks)
+                    s_scale[(n % kScaleSlots) * kBlocks + id] = make_float2(isinf(mine.x) ? NAN : mine.x, mine.y);
 #pragma unroll 1
                 for (int key = id; key < kBN; key += 32 * C::CONV)
                     convert(from + cs * C::CTILE, to + s * TILE, key, is_v && key >= left);
