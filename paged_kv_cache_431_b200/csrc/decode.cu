@@ -31,6 +31,8 @@
 //     partials; decode_reduce merges them with the log-sum-exp rule.  The shared-prefix
 //     (cascade) form starts the partitions after the prefix and merges them with the
 //     prefix's partials written by the tensor-core prefill kernel.
+#include <cfloat>
+
 #include "decode_common.cuh"
 
 namespace pkv {
@@ -248,13 +250,15 @@ decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
                 }
             mx = warp_max_quad(mx);
             const float mn = fmaxf(m_run[hr], mx);   // finite: every tile has a valid token
-            alpha[hr] = ex2(m_run[hr] - mn);
+            // (ragged form: unless all its scores are -inf; they weigh nothing then, where -inf - -inf is NaN)
+            const float ref = RAG ? fmaxf(mn, -FLT_MAX) : mn;
+            alpha[hr] = ex2(m_run[hr] - ref);
             float sum = 0.f;
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    pr[nt][2 * hr + e] = ex2(x[nt][e] - mn);
+                    pr[nt][2 * hr + e] = ex2(x[nt][e] - ref);
                     sum += pr[nt][2 * hr + e];
                 }
             l_run[hr] = l_run[hr] * alpha[hr] + sum;

@@ -30,6 +30,7 @@
 //     reads contiguous code bytes (a dot product does not depend on the order of its
 //     terms); q's fragments use the same assignment.  Output dims are mapped back in
 //     the epilogue.
+#include <cfloat>
 #include <cuda_fp8.h>
 
 #include "decode_common.cuh"
@@ -343,7 +344,10 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
         tbl[j] = blk;
         const size_t si = (size_t)blk * p.H_kv + g;
         tsc[j] = make_float2(p.k_scale[si], p.v_scale[si]);
-        if constexpr (RAG) vs_max = fmaxf(vs_max, tsc[j].y);
+        if constexpr (RAG) {
+            if (isinf(tsc[j].x)) tsc[j].x = NAN;   // its codes of 0 have no product
+            vs_max = fmaxf(vs_max, tsc[j].y);
+        }
     }
     if constexpr (RAG) {
         const int ev = pow2_shift(warp_max(vs_max)) - 13;
@@ -585,13 +589,15 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
             }
             mx = warp_max_quad(mx);
             const float mn = fmaxf(m_run[hr], mx);
-            alpha[hr] = ex2(m_run[hr] - mn);
+            // a tile of scores of -inf alone weighs nothing (-inf - -inf would be NaN)
+            const float ref = RAG ? fmaxf(mn, -FLT_MAX) : mn;
+            alpha[hr] = ex2(m_run[hr] - ref);
             float sum = 0.f;
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    pr[nt][2 * hr + e] = ex2(x[nt][e] - mn);
+                    pr[nt][2 * hr + e] = ex2(x[nt][e] - ref);
                     sum += pr[nt][2 * hr + e];
                 }
             l_run[hr] = l_run[hr] * alpha[hr] + sum;

@@ -21,6 +21,9 @@ TENSOR_CORE = {
     "lone_tile": (8, 2, 7, 150),
     "two_partitions": (8, 2, 20, 1500),
 }
+# 8 and 16 query rows per KV head, with partitions of a few tiles
+WARP_LEVEL = {"eight_rows": (8, 2, 2, 500), "sixteen_rows": (8, 2, 4, 300)}
+FORMS = {**TENSOR_CORE, **WARP_LEVEL}
 
 
 def check_with_nan(out, ref, tol):
@@ -67,13 +70,13 @@ def cross_compare(pool, opool, q, qd, tables, rows, ctx):
 
 
 @pytest.mark.parametrize("value", [NAN, INF, -INF], ids=["nan", "inf", "minus_inf"])
-@pytest.mark.parametrize("form", list(TENSOR_CORE))
+@pytest.mark.parametrize("form", list(FORMS))
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("dt", B16, ids=lambda x: NAMES[x])
 def test_one_key_not_finite(dt, d, form, value):
     """16 sequences, one key of each not finite, at 16 neighbouring positions; the other KV head keeps
     its finite keys.  An infinite element makes the score +inf or -inf by the sign of q's."""
-    pool, opool, q, qd, tables, rows, ctx = cross_case(dt, d, TENSOR_CORE[form], 7000 + dt + d)
+    pool, opool, q, qd, tables, rows, ctx = cross_case(dt, d, FORMS[form], 7000 + dt + d)
     for b in range(16):
         put_key(pool, opool, tables, b, 37 + b, b % 2, (7 * b) % d, value)
     _, ref = cross_compare(pool, opool, q, qd, tables, rows, ctx)
@@ -81,12 +84,12 @@ def test_one_key_not_finite(dt, d, form, value):
     assert share == 0.5 if np.isnan(value) else 0.1 < share < 0.4
 
 
-@pytest.mark.parametrize("form", list(TENSOR_CORE))
+@pytest.mark.parametrize("form", list(FORMS))
 @pytest.mark.parametrize("dt", B16, ids=lambda x: NAMES[x])
 def test_last_keys_and_values_not_finite(dt, form):
     """The last visible key, next to slots beyond the context; a NaN among the values, which reaches
     its own dim alone; query elements that are not finite."""
-    pool, opool, q, qd, tables, rows, ctx = cross_case(dt, 128, TENSOR_CORE[form], 7100 + dt)
+    pool, opool, q, qd, tables, rows, ctx = cross_case(dt, 128, FORMS[form], 7100 + dt)
     for b in range(16):
         if b < 6:
             put_key(pool, opool, tables, b, ctx[b] - 1, 0, 5 * b, (NAN, INF, -INF)[b % 3])
@@ -97,15 +100,15 @@ def test_last_keys_and_values_not_finite(dt, form):
     cross_compare(pool, opool, q, qd, tables, rows, ctx)
 
 
-@pytest.mark.parametrize("form", list(TENSOR_CORE))
+@pytest.mark.parametrize("form", list(FORMS))
 @pytest.mark.parametrize("dt", B16, ids=lambda x: NAMES[x])
 def test_scores_of_minus_infinity(dt, form):
     """Whole tiles, and whole sequences, of scores that are -inf: tiles weigh nothing, a sequence of
     nothing else is 0 / 0."""
-    pool, opool, q, qd, tables, rows, ctx = cross_case(dt, 64, TENSOR_CORE[form], 7200 + dt)
+    pool, opool, q, qd, tables, rows, ctx = cross_case(dt, 64, FORMS[form], 7200 + dt)
     q[..., 11] = q[..., 11].abs() + 1                     # so that -inf in dim 11 is a score of -inf
     for b in range(16):
-        n = (0, 128, 130, ctx[b])[b % 4]
+        n = (0, 128, 130, ctx[b])[b % 4] if form in TENSOR_CORE else (0, 16, 130, ctx[b])[b % 4]
         for pos in range(n):
             put_key(pool, opool, tables, b, pos, b // 8, 11, -INF)
     _, ref = cross_compare(pool, opool, q, qd, tables, rows, ctx)
@@ -113,10 +116,10 @@ def test_scores_of_minus_infinity(dt, form):
 
 
 @pytest.mark.parametrize("dt", pkv.QUANTIZED, ids=lambda x: NAMES[x])
-@pytest.mark.parametrize("form", list(TENSOR_CORE))
+@pytest.mark.parametrize("form", list(FORMS))
 def test_scales_and_codes_not_finite(dt, form):
     """Quantized pools: a block's K or V scale NaN, its K scale infinite, and an e4m3 code that is NaN."""
-    pool, opool, q, qd, tables, rows, ctx = cross_case(dt, 128, TENSOR_CORE[form], 7300 + dt)
+    pool, opool, q, qd, tables, rows, ctx = cross_case(dt, 128, FORMS[form], 7300 + dt)
     for b in range(16):
         blk, head = int(tables[b, 1 + b % 8]), b % 2
         if b % 4 < 2:
@@ -155,6 +158,28 @@ def test_groups_one_key_not_finite(dt, form, where, value):
     ref = reference(opool, q, qd, tables, ctx, range(len(ctx)), 0.125)
     check_with_nan(out, ref, tolerance(opool, q, np.nan_to_num(ref), ctx, 0.125, True))
     assert np.isnan(ref).any()
+
+
+@pytest.mark.parametrize("dt", [pkv.BF16, pkv.INT8], ids=lambda x: NAMES[x])
+def test_groups_suffix_of_minus_infinity(dt):
+    """Sequences whose own tokens, one or more tiles of them, all have scores of -inf keep what their
+    prefix gives (an e4m3 or integer code cannot be infinite: there a block's K scale is NaN)."""
+    sizes, prefix, suffix = [3, 2], [32, 64], [1, 16, 40, 300, 7]
+    pool, opool, q, qd, tables, ctx = groups.case(dt, 64, 8, 2, sizes, prefix, suffix, 7600 + dt)
+    q[..., 11] = q[..., 11].abs() + 1
+    for b in (0, 1, 3):
+        pre = prefix[0] if b < 3 else prefix[1]
+        if dt == pkv.BF16:
+            for pos in range(pre, ctx[b]):
+                put_key(pool, opool, tables, b, pos, 1, 11, -INF)
+        else:
+            blk = int(tables[b, pre // 16])
+            pool.k_scale[0, blk, 1] = opool.k_scale[blk, 1] = NAN
+    out = groups.call(pool, q, tables, ctx, sizes, prefix, suffix, 0.125)
+    torch.cuda.synchronize()
+    ref = reference(opool, q, qd, tables, ctx, range(len(ctx)), 0.125)
+    check_with_nan(out, ref, tolerance(opool, q, np.nan_to_num(ref), ctx, 0.125, True))
+    assert np.isnan(ref).any() == (dt == pkv.INT8)
 
 
 def test_tiny_weights_of_large_values():
