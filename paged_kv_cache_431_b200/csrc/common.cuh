@@ -246,6 +246,20 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// Maxima that keep a NaN, so that a maximum tells whether any of its terms is one.
+__device__ __forceinline__ float fmax_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 __device__ __forceinline__ float warp_max_quad(float v)
 {
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));

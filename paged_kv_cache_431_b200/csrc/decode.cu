@@ -196,7 +196,10 @@ decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
         for (int hn = 0; hn < NHT; ++hn)
 #pragma unroll
             for (int c = 0; c < 4; ++c) o[mt][hn][c] = 0.f;
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    // ragged form: a running max that starts at the lowest number, so that tiles of scores of -inf alone
+    // weigh nothing (-inf - -inf would be NaN)
+    constexpr float kLowest = RAG ? -FLT_MAX : -INFINITY;
+    float m_run[2] = {kLowest, kLowest}, l_run[2] = {0.f, 0.f};
     const float sl = p.scale_log2;
 
     [[maybe_unused]] const bool upper = GC > 8;   // query rows 8 .. 15 of this warp
@@ -250,15 +253,13 @@ decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
                 }
             mx = warp_max_quad(mx);
             const float mn = fmaxf(m_run[hr], mx);   // finite: every tile has a valid token
-            // (ragged form: unless all its scores are -inf; they weigh nothing then, where -inf - -inf is NaN)
-            const float ref = RAG ? fmaxf(mn, -FLT_MAX) : mn;
-            alpha[hr] = ex2(m_run[hr] - ref);
+            alpha[hr] = ex2(m_run[hr] - mn);
             float sum = 0.f;
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    pr[nt][2 * hr + e] = ex2(x[nt][e] - ref);
+                    pr[nt][2 * hr + e] = ex2(x[nt][e] - mn);
                     sum += pr[nt][2 * hr + e];
                 }
             l_run[hr] = l_run[hr] * alpha[hr] + sum;

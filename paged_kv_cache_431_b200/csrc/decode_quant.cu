@@ -12,9 +12,9 @@
 //     sums), against q split into two signed 8-bit digits per element (q scaled per query
 //     head by a power of two and rounded);
 //   * the other codes are converted to fp16 in registers and fed to mma.sync m16n8k16 (f16
-//     in, fp32 accumulate); q is scaled by a power of two chosen per CTA (its largest |q|
+//     in, fp32 accumulate); q is scaled by a power of two chosen per row (its largest |q|
 //     brought near 2^14, exact, undone in the score) and converted to fp16 once per warp,
-//     so a bf16 q keeps its range:
+//     so a bf16 q keeps its range, and each row its precision whatever the others' size:
 //       - int4 K codes: the code plus its offset (c + 8) is moved into the significand of
 //         an fp16 subnormal (one logic op per pair, exact); the offset's share of every
 //         score, 8 * sum(q), is subtracted once per score, and q is pre-scaled by a power
@@ -258,7 +258,7 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
     constexpr int ROW = Cfg::ROW, SWZ = Cfg::SWZ;
     // int4 K codes enter Q . K^T as subnormals u * 2^-24 with u = c + OFF; odd nibbles enter
     // as 16 u, and their q is pre-divided by 16.  q is pre-scaled by a power of two chosen
-    // per CTA (largest |q| brought near 2^14): for int4 the products then stay well clear of
+    // per row (largest |q| brought near 2^14): for int4 the products then stay well clear of
     // the bottom of the accumulator's range, and for fp8 a bf16 q of any magnitude up to
     // 2^113 fits fp16 (a bf16 q above 65504 would otherwise become inf).  The scaling is
     // exact and is undone, with the offset, in the score.
@@ -391,23 +391,24 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
     constexpr int KS8 = D / 32;
     uint32_t qa8[KI8 ? 2 : 1][KI8 ? KS8 : 1][4];
     float qoff[2] = {0.f, 0.f};
-    int eq = 0;   // q is multiplied by 2^eq, which brings max |q| to [2^13, 2^14)
-    int eqr[2] = {0, 0};   // int8: the same per query row (rows r and r + 8)
+    int eq[2] = {0, 0};   // q is multiplied by 2^eq, which brings max |q| of rows r and r + 8 to [2^13, 2^14)
+    bool finite[2];       // whether all of the row's q is
     {
         const bool bf = p.q_bf16;
-        const uint16_t* qh = static_cast<const uint16_t*>(p.q) + ((size_t)b * p.H_q + hbase) * D;
         auto as_float = [&](uint16_t u) -> float {
             return bf ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
         };
-        // ragged form: the lane's D/4 dims from qd * (D/4) of its two query rows, in 16-byte loads
-        [[maybe_unused]] uint32_t qw[RAG ? 2 : 1][RAG ? D / 8 : 1];
-        if constexpr (RAG) {
+        // the lane's D/4 dims from qd * (D/4) of its two query rows, loaded once (the ragged form's q is
+        // 16-byte aligned, the plain form's 4)
+        uint32_t qw[NHT][D / 8];
 #pragma unroll
-            for (int hr = 0; hr < NHT; ++hr) {
-                const bool in = r + 8 * hr < GC;
+        for (int hr = 0; hr < NHT; ++hr) {
+            const int row = r + 8 * hr;
+            const bool in = row < GC;
+            if constexpr (RAG) {
                 const uint4* src = reinterpret_cast<const uint4*>(
-                    static_cast<const uint16_t*>(p.q) +
-                    (in ? ragged_row(it, p.G, p.H_q, g, 16 * hg + r + 8 * hr) : 0) * D + qd * (D / 4));
+                    static_cast<const uint16_t*>(p.q) + (in ? ragged_row(it, p.G, p.H_q, g, 16 * hg + row) : 0) * D +
+                    qd * (D / 4));
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
                     const uint4 u = in ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
@@ -416,54 +417,42 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
                     qw[hr][4 * i + 2] = u.z;
                     qw[hr][4 * i + 3] = u.w;
                 }
+            } else {
+                const uint32_t* src = reinterpret_cast<const uint32_t*>(
+                    static_cast<const uint16_t*>(p.q) + ((size_t)b * p.H_q + hbase + (in ? row : 0)) * D + qd * (D / 4));
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) qw[hr][i] = in ? __ldg(src + i) : 0u;
             }
         }
         // q of row r + 8 hr, dim qd * (D/4) + off
         auto qv = [&](int hr, int off) -> float {
-            if constexpr (RAG) return as_float((uint16_t)(qw[hr][off >> 1] >> (16 * (off & 1))));
-            else return as_float(__ldg(qh + (r + 8 * hr) * D + qd * (D / 4) + off));
+            return as_float((uint16_t)(qw[NHT == 1 ? 0 : hr][off >> 1] >> (16 * (off & 1))));
         };
         const bool r0 = r < GC, r1 = (NHT == 2) && (r + 8 < GC);
-        float qmax = 0.f;
-        if constexpr (RAG) {
+        // the largest |q| of rows r and r + 8: this lane's share of their dims, then the quad's
 #pragma unroll
-            for (int i = 0; i < D / 4; ++i) {   // rows beyond GC are 0
-                qmax = fmaxf(qmax, fabsf(qv(0, i)));
-                if (NHT == 2) qmax = fmaxf(qmax, fabsf(qv(1, i)));
+        for (int hr = 0; hr < 2; ++hr) {
+            float top = 0.f;
+            if (hr < NHT) {   // rows beyond GC are 0
+#pragma unroll
+                for (int i = 0; i < D / 4; ++i) top = fmax_nan(top, fabsf(qv(hr, i)));
             }
-        } else {
-            for (int i = lane; i < GC * D; i += 32) qmax = fmaxf(qmax, fabsf(as_float(__ldg(qh + i))));
+            top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            eq[hr] = pow2_shift(top);
+            finite[hr] = top < INFINITY;
         }
-        eq = pow2_shift(warp_max(qmax));
-        const float qs = pow2f(eq), qo = qs * ODD;
         if constexpr (KI8) {
-            // the largest |q| of rows r and r + 8: this lane's share of their dims, then the quad's
-            float rm[2] = {0.f, 0.f};
-#pragma unroll
-            for (int ks = 0; ks < KS8; ++ks)
-#pragma unroll
-                for (int reg = 0; reg < 4; ++reg) {
-                    const bool live = (reg & 1) ? (NHT == 2 && r + 8 < GC) : (r < GC);
-#pragma unroll
-                    for (int jj = 0; jj < 4; ++jj)
-                        if (live) rm[reg & 1] = fmaxf(rm[reg & 1], fabsf(qv(reg & 1, 8 * ks + 4 * (reg >> 1) + jj)));
-                }
-#pragma unroll
-            for (int hr = 0; hr < 2; ++hr) {
-                rm[hr] = fmaxf(rm[hr], __shfl_xor_sync(0xffffffffu, rm[hr], 1));
-                rm[hr] = fmaxf(rm[hr], __shfl_xor_sync(0xffffffffu, rm[hr], 2));
-                eqr[hr] = pow2_shift(rm[hr]);
-            }
 #pragma unroll
             for (int ks = 0; ks < KS8; ++ks)
 #pragma unroll
                 for (int reg = 0; reg < 4; ++reg) {   // a0: row r, dims +0; a1: r+8, +0; a2: r, +4; a3: r+8, +4
-                    const bool live = (reg & 1) ? (NHT == 2 && r + 8 < GC) : (r < GC);
+                    const bool live = (reg & 1) ? r1 : r0;
                     uint32_t w0 = 0u, w1 = 0u;
 #pragma unroll
                     for (int jj = 0; jj < 4; ++jj) {
                         const int Q = live ? __float2int_rn(qv(reg & 1, 8 * ks + 4 * (reg >> 1) + jj) *
-                                                            pow2f(eqr[reg & 1]))
+                                                            pow2f(eq[reg & 1]))
                                            : 0;
                         const int d1 = (Q + 128) >> 8;
                         w1 |= (uint32_t)(d1 & 0xff) << (8 * jj);
@@ -478,10 +467,11 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
             // dims of the k-slots, counted from the lane's first, qd * (D/4)
             const int d0 = kdim<DT, D>(ks, 0, 0), d1 = kdim<DT, D>(ks, 0, 1);
             const int d2 = kdim<DT, D>(ks, 0, 2), d3 = kdim<DT, D>(ks, 0, 3);
-            qa[ks][0] = r0 ? pack2<false>(qv(0, d0) * qs, qv(0, d1) * qs) : 0u;
-            qa[ks][2] = r0 ? pack2<false>(qv(0, d2) * qo, qv(0, d3) * qo) : 0u;
-            qa[ks][1] = r1 ? pack2<false>(qv(1, d0) * qs, qv(1, d1) * qs) : 0u;
-            qa[ks][3] = r1 ? pack2<false>(qv(1, d2) * qo, qv(1, d3) * qo) : 0u;
+            const float s0 = pow2f(eq[0]), s1 = pow2f(eq[1]);
+            qa[ks][0] = r0 ? pack2<false>(qv(0, d0) * s0, qv(0, d1) * s0) : 0u;
+            qa[ks][2] = r0 ? pack2<false>(qv(0, d2) * (s0 * ODD), qv(0, d3) * (s0 * ODD)) : 0u;
+            qa[ks][1] = r1 ? pack2<false>(qv(1, d0) * s1, qv(1, d1) * s1) : 0u;
+            qa[ks][3] = r1 ? pack2<false>(qv(1, d2) * (s1 * ODD), qv(1, d3) * (s1 * ODD)) : 0u;
         }
         if constexpr (SUBN) {
 #pragma unroll
@@ -493,14 +483,15 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
                     even += e.x + e.y;
                     odd += o.x + o.y;
                 }
-                qoff[hr] = -OFF * pow2f(-eq) * warp_sum_quad(even + odd * (1.f / ODD));
+                qoff[hr] = -OFF * pow2f(-eq[hr]) * warp_sum_quad(even + odd * (1.f / ODD));
             }
         }
     }
-    // log2-domain score = (acc * 2^(24-eq) + qoff) * sl for int4, acc * 2^-eq * sl for int8 / fp8
+    // log2-domain score = (acc * 2^(24-eq) + qoff) * sl for int4, acc * 2^-eq * sl for int8 / fp8; a row
+    // of q that is not finite has no finite score (its digits or fp16 values need not say so)
     float kq[2];   // per query row r (hr 0) and r + 8 (hr 1)
 #pragma unroll
-    for (int hr = 0; hr < 2; ++hr) kq[hr] = KI8 ? pow2f(-eqr[hr]) : pow2f(SUBN ? 24 - eq : -eq);
+    for (int hr = 0; hr < 2; ++hr) kq[hr] = finite[hr] ? pow2f(SUBN ? 24 - eq[hr] : -eq[hr]) : NAN;
 
     float o[Cfg::MT][NHT][4];
 #pragma unroll
@@ -509,7 +500,10 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
         for (int hn = 0; hn < NHT; ++hn)
 #pragma unroll
             for (int c = 0; c < 4; ++c) o[mt][hn][c] = 0.f;
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    // ragged form: a running max that starts at the lowest number, so that tiles of scores of -inf alone
+    // weigh nothing (-inf - -inf would be NaN)
+    constexpr float kLowest = RAG ? -FLT_MAX : -INFINITY;
+    float m_run[2] = {kLowest, kLowest}, l_run[2] = {0.f, 0.f};
 
     [[maybe_unused]] const bool upper = GC > 8;   // query rows 8 .. 15 of this CTA
     int j = 0;
@@ -589,15 +583,13 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
             }
             mx = warp_max_quad(mx);
             const float mn = fmaxf(m_run[hr], mx);
-            // a tile of scores of -inf alone weighs nothing (-inf - -inf would be NaN)
-            const float ref = RAG ? fmaxf(mn, -FLT_MAX) : mn;
-            alpha[hr] = ex2(m_run[hr] - ref);
+            alpha[hr] = ex2(m_run[hr] - mn);
             float sum = 0.f;
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    pr[nt][2 * hr + e] = ex2(x[nt][e] - ref);
+                    pr[nt][2 * hr + e] = ex2(x[nt][e] - mn);
                     sum += pr[nt][2 * hr + e];
                 }
             l_run[hr] = l_run[hr] * alpha[hr] + sum;

@@ -156,20 +156,6 @@ __device__ __forceinline__ float2 exp2_poly(float2 a)
                        __int_as_float(__float_as_int(y.y) + (__float_as_int(t.y) << 23)));
 }
 
-// Maxima that keep a NaN, so that a row maximum tells whether any of its scores is one.
-__device__ __forceinline__ float fmax_nan(float a, float b)
-{
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float fmax3_nan(float a, float b, float c)
-{
-    float r;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((127 + e) << 23); }   // e in [-126, 127]
 
 // Exponent shift that brings x > 0 to [1, 2), kept in [-100, 100]; 0 for x = 0.

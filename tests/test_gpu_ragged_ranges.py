@@ -1,0 +1,83 @@
+"""The ragged operators, and the decode of quantized pools, where magnitudes differ widely within a
+call: query rows, V scales, weights."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from paged_kv_cache_431_b200 import pkv
+from paged_kv_cache_431_b200 import workloads as wl
+from tests import test_gpu_cross as cross
+from tests.ragged_helpers import DEV, NAMES, check, make_pool, reference, tables_for, tolerance
+
+pytestmark = pytest.mark.gpu
+
+# query rows per KV head: warp level with 8 and 16, tcgen05 with the rows four times, twice, once in a
+# tile (quantized pools), and with shared tiles
+ROWS = [[2], [4], [7], [14], [25], [90]]
+
+
+def call(pool, q, rows, tables, ctx, scale):
+    out = pkv.paged_cross_attn(pool, 0, q.to(DEV), cross.starts_of(rows).to(DEV), tables.to(DEV),
+                               torch.tensor(ctx, dtype=torch.int32, device=DEV), scale, max(rows), max(ctx))
+    torch.cuda.synchronize()
+    assert pkv.read_device_status(pool) == 0
+    return out
+
+
+@pytest.mark.parametrize("rows", ROWS, ids=lambda r: f"{r[0]}rows")
+@pytest.mark.parametrize("dt", [pkv.BF16, *pkv.QUANTIZED], ids=lambda x: NAMES[x])
+def test_rows_2_40_apart_in_size_keep_their_precision(dt, rows):
+    """Every other row 2^40 times smaller, once with a scale that suits the small ones, once one that
+    suits the large ones; the suited rows are compared.  Zero in place of the small rows would be off by
+    far more than the tolerance (checked on the oracle)."""
+    ctx = [700]
+    pool, opool, q, qd, tables = cross.case(dt, 128, 4, 1, rows, ctx, 8000 + dt + rows[0])
+    small = torch.arange(rows[0]) % 2 == 0
+    q[small] *= 2.0 ** -40
+    for some, scale in ((small, 0.1 * 2.0 ** 40), (~small, 0.1)):
+        out = call(pool, q, rows, tables, ctx, scale)
+        qs, n = q[some].contiguous(), int(some.sum())
+        ref = reference(opool, qs, qd, tables, ctx, [0] * n, scale)
+        tol = tolerance(opool, qs, ref, ctx, scale, True)
+        check(out[some], ref, tol)
+        none = reference(opool, torch.zeros_like(qs), qd, tables, ctx, [0] * n, scale)
+        assert (np.abs(none - ref) > tol).mean() > 0.5
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")], ids=["nan", "inf", "minus_inf"])
+@pytest.mark.parametrize("rows", ROWS, ids=lambda r: f"{r[0]}rows")
+@pytest.mark.parametrize("dt", pkv.QUANTIZED, ids=lambda x: NAMES[x])
+def test_rows_not_finite_leave_the_others_alone(dt, rows, value):
+    """A row of q with an element that is not finite is NaN, its neighbours are as without it."""
+    ctx = [300]
+    pool, opool, q, qd, tables = cross.case(dt, 64, 4, 1, rows, ctx, 8050 + dt + rows[0])
+    q[1, 2, 5] = value
+    out = call(pool, q, rows, tables, ctx, 0.1)
+    assert torch.isnan(out[1, 2]).all()
+    clean = q.clone()
+    clean[1, 2] = 0
+    ref = reference(opool, clean, qd, tables, ctx, [0] * rows[0], 0.1)
+    tol = tolerance(opool, clean, ref, ctx, 0.1, True)
+    out[1, 2], ref[1, 2], tol[1, 2] = 0, 0, 1
+    check(out, ref, tol)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")], ids=["nan", "inf", "minus_inf"])
+@pytest.mark.parametrize("dt", pkv.QUANTIZED, ids=lambda x: NAMES[x])
+def test_decode_heads_not_finite_leave_the_others_alone(dt, value):
+    """The same for the heads of one sequence in the plain decode."""
+    g = wl.generator(8090 + dt)
+    ctx = [300, 90]
+    tables, N = tables_for(ctx, g)
+    pool, opool = make_pool(tables, ctx, N, 2, 128, dt, g)
+    q = wl.normal((2, 8, 128), torch.bfloat16, g)
+    q[1, 2, 5] = value
+    lens = torch.tensor(ctx, dtype=torch.int32)
+    out = pkv.paged_decode_attn(pool, 0, q.to(DEV), tables.to(DEV), lens.to(DEV), 0.1, max(ctx)).cpu().double().numpy()
+    clean = q.clone()
+    clean[1, 2] = 0
+    ref = oracle.paged_decode(opool, clean, pkv.BF16, tables, lens, np.float32(0.1))
+    assert np.isnan(out[1, 2]).all()
+    out[1, 2] = ref[1, 2]
+    assert np.abs(out - ref).max() <= 2e-3
