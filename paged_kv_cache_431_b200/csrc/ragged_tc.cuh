@@ -43,6 +43,7 @@ constexpr float kSlack = 8.f;                    // log2 units the running max m
 constexpr uint32_t kTmemCols = 512;              // tile x: S and P at 256x, O at 256x + 128
 constexpr int kPolyEvery = 4;                    // of so many pairs of exponentials, one is a polynomial
 constexpr float kTiny = 1.17549435e-38f;
+constexpr float kHuge = 1048576.f;               // scores (log2 units) whose rounding, 2^-4, is still no matter
 constexpr int kScaleSlots = 4;                   // key tiles whose scales are kept
 
 template <int D, int DT, bool PAIR>
@@ -441,6 +442,11 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
         // well (a NaN stays: it is the caller's scale)
         sl = fmax_nan(sl, kTiny);
         float m_used = -INFINITY, l_run = 0.f;
+        // Huge scores: factor S - m in one step leaves the rounding of the maximum, which passes the
+        // exponents' range from 2^28 on.  There the product is rounded by itself, as the maximum's was, so
+        // that the largest score gives 0.  (Quantized pools always do so: in two steps 413 us instead of
+        // 372 on 4 x 1,024 rows of head dim 64.)
+        bool huge = false;
         for (int t = 0; ok && t < nx; ++t) {
             const int n = seq(x, t);
             ok = wait(bars.s_full[x], t & 1);
@@ -504,7 +510,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 }
                 mx = fmax3_nan(mx, m2[0], m2[1]);
             }
-            if constexpr (!C::QUANT) mx *= sl;
+            if constexpr (!C::QUANT) mx = __fmul_rn(mx, sl);
             // a NaN becomes the row's maximum, and so reaches its sum; one of +inf is looked for behind the loop
             const float m_new = mx <= m_used + kSlack ? m_used : mx;
             const float alpha = m_used == -INFINITY ? 0.f : ex2(m_used - m_new);
@@ -515,9 +521,10 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 if (!ok) break;
                 tc_fence_after();
             }
-            if (t > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                if constexpr (!C::QUANT) huge = __any_sync(0xffffffffu, fabsf(m_new) > kHuge);
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
+                for (int c = 0; t > 0 && c < D / 32; ++c) {
                     float o[32];
                     tmem_ld32(tO + 32 * c, o);
                     tmem_wait_ld();
@@ -553,6 +560,13 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 else if (t > 0) ok = wait(turn, (t - 1) & 1);
                 if (!ok) break;
             }
+            if constexpr (!C::QUANT) {
+                if (huge) {
+#pragma unroll
+                    for (int j = 0; j < kBN; ++j) v[j >> 5][j & 31] = __fmul_rn(v[j >> 5][j & 31], sl);
+                }
+            }
+            const float fac = huge ? 1.f : sl;
             // P = 2^(factor S - m) in 16 bits, packed into the tile's first 64 columns, in two halves
             const float2 mref2 = make_float2(-mref, -mref);
             float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -570,14 +584,16 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
                 uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    float f = sl;
+                    float f = fac;
                     [[maybe_unused]] float vm = 1.f;
                     if constexpr (C::QUANT) {
                         const float2 kv = sc[2 * c + (e >> 3)];
                         f = fmaxf(sl * kv.x, kTiny);
                         vm = v_mul * kv.y;
                     }
-                    const float2 a = ffma2(make_float2(u[2 * e], u[2 * e + 1]), make_float2(f, f), mref2);
+                    const float2 s2 = make_float2(u[2 * e], u[2 * e + 1]), f2 = make_float2(f, f);
+                    // (+ 0: a product alone would be fused with the sum all the same)
+                    const float2 a = C::QUANT ? fadd2(ffma2(s2, f2, make_float2(0.f, 0.f)), mref2) : ffma2(s2, f2, mref2);
                     float2 pp;
                     // some pairs take the FMA pipe, so that it shares the exponentials with the
                     // special-function unit

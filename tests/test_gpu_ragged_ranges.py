@@ -81,3 +81,28 @@ def test_decode_heads_not_finite_leave_the_others_alone(dt, value):
     assert np.isnan(out[1, 2]).all()
     out[1, 2] = ref[1, 2]
     assert np.abs(out - ref).max() <= 2e-3
+
+
+@pytest.mark.parametrize("gain", [2.0 ** 20, 2.0 ** 60], ids=["2^20", "2^60"])
+@pytest.mark.parametrize("rows", ROWS, ids=lambda r: f"{r[0]}rows")
+@pytest.mark.parametrize("dt", list(NAMES), ids=lambda x: NAMES[x])
+def test_huge_scores_leave_one_key(dt, rows, gain):
+    """Scores of 10^6 and 10^18 times the usual size: a row takes the values of its best key (rows whose
+    two best keys are closer than the scores' own rounding may mix them, and are only finite)."""
+    ctx = [700]
+    pool, opool, q, qd, tables = cross.case(dt, 128, 4, 1, rows, ctx, 8100 + dt + rows[0])
+    scale = 0.1 * gain
+    out = call(pool, q, rows, tables, ctx, scale)
+    assert torch.isfinite(out).all()
+    blocks = tables[0, :-(-ctx[0] // 16)].long()
+    k = torch.as_tensor(opool.dequant("k"))[blocks].transpose(1, 2).reshape(-1, 128)[:ctx[0]]
+    best = (q.double() @ k.T).topk(2, dim=-1).values
+    # fp32 sums of 128 terms: (128 + 2) 2^-24 |q| |k|; quantized pools' q: 2^-14 / sqrt(128) of it more
+    err = q.double().norm(dim=-1) * k.norm(dim=-1).max() * (130 * 2.0 ** -24 + 2.0 ** -14 / 128 ** 0.5)
+    clear = ((best[..., 0] - best[..., 1] - 2 * err) * scale > 40).numpy()
+    assert clear.mean() > 0.9
+    ref = reference(opool, q, qd, tables, ctx, [0] * rows[0], scale)
+    # a weight of 1, rounded nowhere, times a value whose scale is rounded into P; and the output's half step
+    got = out.cpu().double().numpy()
+    bound = torch.finfo(q.dtype).eps / 2 * np.abs(ref) + 2.0 ** -11 * np.abs(ref) + 2.0 ** -24
+    assert (np.abs(got - ref) <= bound)[clear].all()
