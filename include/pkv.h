@@ -379,6 +379,9 @@ PKV_API size_t paged_cross_workspace_bytes(pkv_pool_t pool, int total_rows, int 
  *   max_rows, max_context_len [host]: bounds of a sequence's rows and of context_lens (the latter
  *        at most 2^30).
  *   workspace [device]: paged_cross_workspace_bytes(...) bytes, 16-byte aligned.
+ * Quantized pools: V scales of one sequence and KV head may differ by factors up to 2^20 without loss; a
+ * row whose weight lies on blocks with smaller ones loses bits (a weight times its V scale is held in steps
+ * of at most 2^-30 of the largest V scale).
  * All pool dtypes, head dims and group sizes.  On the device: lengths and row_starts out of range
  * are clipped to the bounds and set PKV_DEV_BAD_LENGTH (rows past max_rows are not written).
  */

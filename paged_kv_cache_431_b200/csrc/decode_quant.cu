@@ -331,8 +331,9 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
     float2* tsc = reinterpret_cast<float2*>(smem + Cfg::BODY);
     int* tbl = reinterpret_cast<int*>(tsc + p.part_tokens / kBlock);
-    // ragged form: the V scales of the partition times 2^ev, which brings the largest to [1, 2), so
-    // that P times a scale keeps fp16's range whatever the pool's magnitude (undone in the epilogue)
+    // ragged form: the V scales of the partition times 2^ev, which brings the largest to [2^13, 2^14), so
+    // that P (at most 1) times a scale keeps fp16's range whatever the pool's magnitude, and its 11 bits
+    // on blocks whose V scale is down to 2^-27 of the largest (undone in the epilogue)
     float v_unit = 1.f;
     float vs_max = 0.f;
     for (int j = lane; j < ntiles; j += 32) {
@@ -350,7 +351,7 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
         }
     }
     if constexpr (RAG) {
-        const int ev = pow2_shift(warp_max(vs_max)) - 13;
+        const int ev = pow2_shift(warp_max(vs_max));
         for (int j = lane; j < ntiles; j += 32) tsc[j].y *= pow2f(ev);
         v_unit = pow2f(-ev);
     }

@@ -434,7 +434,9 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
         if constexpr (C::QUANT) {
             ok = wait(bars.q_full, 0);
             sl *= s_rowscale[(PAIR ? 0 : x * kBM) + r];
-            const int e = unit_shift(__int_as_float(s_vmax));
+            // the largest V scale to [2^6, 2^7): P, up to 2^8, times it then stays within fp16, and keeps its
+            // 11 bits on blocks whose V scale is down to 2^-20 of that
+            const int e = unit_shift(__int_as_float(s_vmax)) + 6;
             v_mul = exp2_int(e);
             v_unit = exp2_int(-e);
         }

@@ -106,3 +106,42 @@ def test_huge_scores_leave_one_key(dt, rows, gain):
     got = out.cpu().double().numpy()
     bound = torch.finfo(q.dtype).eps / 2 * np.abs(ref) + 2.0 ** -11 * np.abs(ref) + 2.0 ** -24
     assert (np.abs(got - ref) <= bound)[clear].all()
+
+
+def steer(pool, opool, blocks, d, up):
+    """Codes of K's dim 0 in the listed blocks: the largest positive one, or the largest negative one."""
+    code = {pkv.INT8: (0x7F, 0x81), pkv.INT4: (0x7, 0x9), pkv.FP8E4M3: (0x7E, 0xFE)}[opool.dtype][0 if up else 1]
+    for blk in blocks:
+        if opool.dtype == pkv.INT4:
+            opool.k[blk, :, :, 0] = (opool.k[blk, :, :, 0] & 0xF0) | code
+        else:
+            opool.k[blk, :, :, 0] = code
+        opool.k_scale[blk] = opool.k_scale[blocks[0]]
+        pool.k_data[0, blk] = torch.as_tensor(opool.k[blk])
+        pool.k_scale[0, blk] = torch.as_tensor(opool.k_scale[blk])
+
+
+@pytest.mark.parametrize("ratio", [2.0 ** -20, 2.0 ** -12], ids=["2^-20", "2^-12"])
+@pytest.mark.parametrize("rows", ROWS, ids=lambda r: f"{r[0]}rows")
+@pytest.mark.parametrize("dt", pkv.QUANTIZED, ids=lambda x: NAMES[x])
+def test_weight_on_blocks_with_small_v_scales(dt, rows, ratio):
+    """Every other block's V scale 2^-20 of its neighbour's, the rows' weight on these blocks: the output
+    is as exact as if the others, which weigh less than 2^-60, were not there."""
+    ctx, d = [700], 128
+    pool, opool, q, qd, tables = cross.case(dt, d, 4, 1, rows, ctx, 8300 + dt + rows[0], gain=6.0)
+    blocks = tables[0, :-(-ctx[0] // 16)].tolist()
+    for blk in blocks[::2]:
+        opool.v_scale[blk] *= ratio
+        pool.v_scale[0, blk] = torch.as_tensor(opool.v_scale[blk])
+    steer(pool, opool, blocks[::2], d, True)
+    steer(pool, opool, blocks[1::2], d, False)
+    q[..., 0] = 256.0
+    scale = d ** -0.5
+    out = call(pool, q, rows, tables, ctx, scale)
+    ref = reference(opool, q, qd, tables, ctx, [0] * rows[0], scale)
+    small = opool.copy()
+    small.v_scale[blocks[1::2]] = 0
+    near = reference(small, q, qd, tables, ctx, [0] * rows[0], scale)
+    tol = tolerance(small, q, near, ctx, scale, True)
+    assert np.abs(ref - near).max() < 1e-3 * tol.min()
+    check(out, ref, tol)
