@@ -331,10 +331,9 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
     float2* tsc = reinterpret_cast<float2*>(smem + Cfg::BODY);
     int* tbl = reinterpret_cast<int*>(tsc + p.part_tokens / kBlock);
-    // ragged form: the V scales of the partition times 2^ev, which brings the largest to [2^13, 2^14), so
-    // that P (at most 1) times a scale keeps fp16's range whatever the pool's magnitude, and its 11 bits
-    // on blocks whose V scale is down to 2^-27 of the largest (undone in the epilogue)
-    float v_unit = 1.f;
+    // the V scales of the partition times 2^ev, which brings the largest to [2^13, 2^14), so that P (at
+    // most 1) times a scale keeps fp16's range whatever the pool's magnitude, and its 11 bits (22 in two
+    // parts) on blocks whose V scale is down to 2^-27 (2^-16) of the largest (undone in the epilogue)
     float vs_max = 0.f;
     for (int j = lane; j < ntiles; j += 32) {
         int blk = trow[j];
@@ -345,16 +344,11 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
         tbl[j] = blk;
         const size_t si = (size_t)blk * p.H_kv + g;
         tsc[j] = make_float2(p.k_scale[si], p.v_scale[si]);
-        if constexpr (RAG) {
-            if (isinf(tsc[j].x)) tsc[j].x = NAN;   // its codes of 0 have no product
-            vs_max = fmaxf(vs_max, tsc[j].y);
-        }
+        if (RAG && isinf(tsc[j].x)) tsc[j].x = NAN;   // its codes of 0 have no product
+        vs_max = fmaxf(vs_max, tsc[j].y);
     }
-    if constexpr (RAG) {
-        const int ev = pow2_shift(warp_max(vs_max));
-        for (int j = lane; j < ntiles; j += 32) tsc[j].y *= pow2f(ev);
-        v_unit = pow2f(-ev);
-    }
+    const int ev = pow2_shift(warp_max(vs_max));
+    const float v_up = pow2f(ev), v_unit = pow2f(-ev);
     if (lane == 0) {
         for (int s = 0; s < STAGES; ++s) mbar_init(smem_u32(&bars[s]), 1);
         mbar_fence_init();
@@ -525,6 +519,7 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
         // compiled schedule measured faster that way)
         constexpr bool SKIP_MASK = DT != PKV_INT4;
         const float2 sc_kv = tsc[j];
+        const float vs = sc_kv.y * v_up;
 
         // S = Q . K^T, token 8 nt + r of the tile in n-tile nt
         float sc[2][4];
@@ -619,7 +614,7 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
             if (RAG && hn == 1 && !upper) continue;
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-                const float p0 = pr[nt][2 * hn] * sc_kv.y, p1 = pr[nt][2 * hn + 1] * sc_kv.y;
+                const float p0 = pr[nt][2 * hn] * vs, p1 = pr[nt][2 * hn + 1] * vs;
                 bh[hn][nt] = pack2<false>(p0, p1);
                 if constexpr (!RAG) {   // the ragged output is 16-bit: one part of P is as exact as it is
                     const float2 back = unpack2<false>(bh[hn][nt]);
@@ -693,10 +688,8 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
             inv_lo = 1.f / la;
             inv_hi = 1.f / lb;
         }
-        if constexpr (RAG) {
-            inv_lo *= v_unit;
-            inv_hi *= v_unit;
-        }
+        inv_lo *= v_unit;
+        inv_hi *= v_unit;
         const int h0 = 8 * hn + 2 * qd;
 #pragma unroll
         for (int mt = 0; mt < Cfg::MT; ++mt) {

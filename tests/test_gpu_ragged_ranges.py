@@ -145,3 +145,23 @@ def test_weight_on_blocks_with_small_v_scales(dt, rows, ratio):
     tol = tolerance(small, q, near, ctx, scale, True)
     assert np.abs(ref - near).max() < 1e-3 * tol.min()
     check(out, ref, tol)
+
+
+@pytest.mark.parametrize("spread", [1e-9, 1e-6, 1e6], ids=["1e-9", "1e-6", "1e6"])
+@pytest.mark.parametrize("H_q,H_kv", [(8, 2), (24, 2), (32, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dt", pkv.QUANTIZED, ids=lambda x: NAMES[x])
+def test_decode_of_small_and_large_pools(dt, d, H_q, H_kv, spread):
+    """The plain decode over pools whose scales are far from 1, in one partition and in several (the
+    output's bound of 2e-3 in proportion to the pool's magnitude)."""
+    g = wl.generator(8400 + dt + d + H_q)
+    ctx = [700, 33, 1, 5000]
+    tables, N = tables_for(ctx, g)
+    pool, opool = make_pool(tables, ctx, N, H_kv, d, dt, g, spread)
+    q = wl.normal((len(ctx), H_q, d), torch.bfloat16, g)
+    lens = torch.tensor(ctx, dtype=torch.int32)
+    scale = d ** -0.5 / spread
+    ref = oracle.paged_decode(opool, q, pkv.BF16, tables, lens, np.float32(scale))
+    for part in (0, 512):
+        out = pkv.paged_decode_attn(pool, 0, q.to(DEV), tables.to(DEV), lens.to(DEV), scale, max(ctx), partition_tokens=part)
+        assert np.abs(out.cpu().double().numpy() - ref).max() <= 2e-3 * spread
