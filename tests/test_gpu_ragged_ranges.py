@@ -148,7 +148,7 @@ def test_weight_on_blocks_with_small_v_scales(dt, rows, ratio):
 
 
 @pytest.mark.parametrize("spread", [1e-9, 1e-6, 1e6], ids=["1e-9", "1e-6", "1e6"])
-@pytest.mark.parametrize("H_q,H_kv", [(8, 2), (24, 2), (32, 2)])
+@pytest.mark.parametrize("H_q,H_kv", [(8, 2), (16, 2), (24, 2), (32, 2)])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("dt", pkv.QUANTIZED, ids=lambda x: NAMES[x])
 def test_decode_of_small_and_large_pools(dt, d, H_q, H_kv, spread):
