@@ -272,8 +272,8 @@ def kv_append(pool: KVPool, layer: int, k: torch.Tensor, v: torch.Tensor, slot_m
 
 
 # What the calls below share: all tensors on the pool's device, which is made current for the
-# launch if it is not; plain integers as pointers (ctypes converts them fastest); a workspace or
-# output taken from torch's allocator stays reserved for the stream that the call was given.
+# launch if it is not; plain integers as pointers (ctypes converts them fastest); workspaces and
+# outputs taken from torch's allocator for the stream that the call was given.
 
 def _device_index(pool: KVPool, *tensors) -> int:
     idx = pool.__dict__.get("_dev")
@@ -295,10 +295,21 @@ def _stream_of(stream, idx: int) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _keep(t: torch.Tensor, stream, idx: int) -> torch.Tensor:
+def _empty(shape, dtype, stream, idx: int, result: bool = True) -> torch.Tensor:
+    """A tensor for a call on `stream`.  Torch's allocator hands out blocks whose last work is still
+    queued on the stream they are allocated for, so that has to be the call's; a result the caller reads
+    from the current stream stays reserved until that has passed its release."""
     if stream is not None:
-        t.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), idx))
-    return t
+        now = torch.cuda.current_stream(idx)
+        raw = _stream_of(stream, idx)
+        if raw != now.cuda_stream:
+            own = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw, idx)
+            with torch.cuda.stream(own):
+                t = torch.empty(shape, dtype=dtype, device=idx)
+            if result:
+                t.record_stream(now)
+            return t
+    return torch.empty(shape, dtype=dtype, device=idx)
 
 
 def _ws(workspace, need: int, stream, idx: int):
@@ -306,7 +317,7 @@ def _ws(workspace, need: int, stream, idx: int):
     if workspace is None:
         if not need:
             return None, 0, 0
-        workspace = _keep(torch.empty(need, dtype=torch.uint8, device=idx), stream, idx)
+        workspace = _empty(need, torch.uint8, stream, idx, result=False)
     elif not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -362,7 +373,7 @@ def kv_append_rope(pool: KVPool, layer: int, q: torch.Tensor | None, k: torch.Te
         H_q = q.shape[1]
         qp, qs = _rows(q, T, H_q, d, "q")
         if q_out is None:
-            q_out = _keep(torch.empty(T, H_q, d, dtype=q.dtype, device=idx), stream, idx)
+            q_out = _empty((T, H_q, d), q.dtype, stream, idx)
         elif q_out.dtype is not q.dtype:
             raise ValueError("q_out must have q's dtype")
         qop, qos = _rows(q_out, T, H_q, d, "q_out")
@@ -443,7 +454,7 @@ def _ragged_rows(pool: KVPool, q, out, stream, idx: int):
     if q.dim() != 3 or not q.is_contiguous() or q.shape[2] != pool.head_dim:
         raise ValueError(f"q: expected a contiguous [rows, H_q, {pool.head_dim}] tensor")
     if out is None:
-        return _keep(torch.empty_like(q), stream, idx)
+        return _empty(q.shape, q.dtype, stream, idx)
     if out.dtype is not q.dtype or out.shape != q.shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of q's shape and dtype")
     return out
