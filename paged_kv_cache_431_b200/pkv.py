@@ -154,6 +154,32 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, idx: int) -> int:
+    if stream is None:
+        return _raw_stream(idx) if _raw_stream is not None else torch.cuda.current_stream(idx).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _empty(shape, dtype, stream, idx, result: bool = True) -> torch.Tensor:
+    """A tensor for a call on `stream`.  Torch's allocator hands out blocks whose last work is still
+    queued on the stream they are allocated for, so that has to be the call's; a result the caller reads
+    from the current stream stays reserved until that has passed its release."""
+    if stream is not None:
+        now = torch.cuda.current_stream(idx)
+        raw = _stream_of(stream, idx)
+        if raw != now.cuda_stream:
+            own = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw, idx)
+            with torch.cuda.stream(own):
+                t = torch.empty(shape, dtype=dtype, device=idx)
+            if result:
+                t.record_stream(now)
+            return t
+    return torch.empty(shape, dtype=dtype, device=idx)
+
+
 def row_bytes(kv_dtype: int, head_dim: int) -> int:
     return {F16: 2 * head_dim, BF16: 2 * head_dim, INT8: head_dim, FP8E4M3: head_dim, INT4: head_dim // 2}[kv_dtype]
 
@@ -265,7 +291,7 @@ def kv_append(pool: KVPool, layer: int, k: torch.Tensor, v: torch.Tensor, slot_m
     T = slot_mapping.shape[0]
     need = kv_append_workspace_bytes(pool, T)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=k.device)
+        workspace = _empty(need, torch.uint8, stream, k.device, result=False)
     _check(lib().kv_append(pool.handle, layer, _ptr(k), _ptr(v), _dtype_code(k), _ptr(slot_mapping), T,
                            _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None
                            else 0, _stream(stream)), "kv_append")
@@ -284,32 +310,6 @@ def _device_index(pool: KVPool, *tensors) -> int:
         if t is not None and t.get_device() != idx:
             raise ValueError("expected CUDA tensors on the pool's device")
     return idx
-
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream_of(stream, idx: int) -> int:
-    if stream is None:
-        return _raw_stream(idx) if _raw_stream is not None else torch.cuda.current_stream(idx).cuda_stream
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _empty(shape, dtype, stream, idx: int, result: bool = True) -> torch.Tensor:
-    """A tensor for a call on `stream`.  Torch's allocator hands out blocks whose last work is still
-    queued on the stream they are allocated for, so that has to be the call's; a result the caller reads
-    from the current stream stays reserved until that has passed its release."""
-    if stream is not None:
-        now = torch.cuda.current_stream(idx)
-        raw = _stream_of(stream, idx)
-        if raw != now.cuda_stream:
-            own = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw, idx)
-            with torch.cuda.stream(own):
-                t = torch.empty(shape, dtype=dtype, device=idx)
-            if result:
-                t.record_stream(now)
-            return t
-    return torch.empty(shape, dtype=dtype, device=idx)
 
 
 def _ws(workspace, need: int, stream, idx: int):
@@ -408,10 +408,10 @@ def paged_decode_attn(pool: KVPool, layer: int, q: torch.Tensor, block_tables: t
     sliding_window > 0: the query sees only the last sliding_window positions."""
     B, H_q, d = q.shape
     if out is None:
-        out = torch.empty(B, H_q, d, dtype=torch.float32, device=q.device)
+        out = _empty((B, H_q, d), torch.float32, stream, q.device)
     need = paged_decode_workspace_bytes(pool, B, H_q, max_context_len, engine, partition_tokens, sliding_window)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, torch.uint8, stream, q.device, result=False)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib().paged_decode_attn(pool.handle, layer, _ptr(q), _dtype_code(q), _ptr(block_tables),
                                    block_tables.shape[1], _ptr(context_lens), B, H_q, max_context_len,
@@ -437,11 +437,11 @@ def paged_decode_attn_cascade(pool: KVPool, layer: int, q: torch.Tensor, block_t
     fn = lib().paged_decode_attn_cascade
     B, H_q, d = q.shape
     if out is None:
-        out = torch.empty(B, H_q, d, dtype=torch.float32, device=q.device)
+        out = _empty((B, H_q, d), torch.float32, stream, q.device)
     need = paged_decode_cascade_workspace_bytes(pool, B, H_q, max_context_len, shared_prefix_len, engine,
                                                 partition_tokens)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, torch.uint8, stream, q.device, result=False)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(fn(pool.handle, layer, _ptr(q), _dtype_code(q), _ptr(block_tables), block_tables.shape[1],
               _ptr(context_lens), B, H_q, max_context_len, shared_prefix_len, float(scale), _ptr(out),
@@ -546,7 +546,7 @@ def paged_decode_attn_noalloc(pool: KVPool, layer: int, q: torch.Tensor, block_t
     fn = lib().paged_decode_attn_noalloc
     B, H_q, d = q.shape
     if out is None:
-        out = torch.empty(B, H_q, d, dtype=torch.float32, device=q.device)
+        out = _empty((B, H_q, d), torch.float32, stream, q.device)
     _check(fn(pool.handle, layer, _ptr(q), _dtype_code(q), _ptr(block_tables), block_tables.shape[1],
               _ptr(context_lens), B, H_q, max_context_len, float(scale), _ptr(out),
               _opts(engine, partition_tokens, sliding_window), _stream(stream)), "paged_decode_attn_noalloc")
@@ -560,7 +560,7 @@ def paged_prefill_chunk_attn(pool: KVPool, layer: int, q: torch.Tensor, block_ta
     (sliding_window > 0: each row sees only the last sliding_window positions up to itself)."""
     C, H_q, d = q.shape
     if out is None:
-        out = torch.empty(C, H_q, d, dtype=torch.float32, device=q.device)
+        out = _empty((C, H_q, d), torch.float32, stream, q.device)
     if sliding_window == 0:
         _check(lib().paged_prefill_chunk_attn(pool.handle, layer, _ptr(q), _dtype_code(q), _ptr(block_table),
                                               block_table.shape[-1], ctx_before, C, H_q, float(scale), _ptr(out),

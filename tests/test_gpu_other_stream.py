@@ -67,3 +67,26 @@ def test_append_rope(raw):
     table = torch.randn(T, 128, device=DEV)
     beside_queued_work(lambda s: pkv.kv_append_rope(pool, 0, q, k, v, pos, table, pos, stream=s),
                        [q.numel() * 2, pkv.kv_append_rope_workspace_bytes(pool, T)], raw)
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_decode_and_append(raw):
+    """The calls that were there before: their workspaces, let go of while the call's stream still runs,
+    and outputs."""
+    T, g = 600, wl.generator(9300)
+    pool = pkv.KVPool.allocate(1, 64, 2, 128, pkv.INT8)
+    k, v = (wl.normal((T, 2, 128), torch.bfloat16, g).to(DEV) for _ in range(2))
+    slots = torch.arange(T, dtype=torch.int32, device=DEV)
+
+    pkv.kv_append(pool, 0, k, v, slots)
+    q = wl.normal((8, 8, 128), torch.bfloat16, g).to(DEV)
+    tables = torch.arange(32, dtype=torch.int32, device=DEV).repeat(8, 1)
+    lens = torch.full((8,), 500, dtype=torch.int32, device=DEV)
+    need = pkv.paged_decode_workspace_bytes(pool, 8, 8, 500, partition_tokens=64)
+    beside_queued_work(lambda s: pkv.paged_decode_attn(pool, 0, q, tables, lens, 0.1, 500, partition_tokens=64, stream=s),
+                       [q.numel() * 4, need], raw)
+    want = [t.clone() for t in (pool.k_data, pool.v_data, pool.k_scale, pool.v_scale)]
+    beside_queued_work(lambda s: (pkv.kv_append(pool, 0, k, v, slots, stream=s), k)[1],
+                       [pkv.kv_append_workspace_bytes(pool, T)], raw)
+    for t, w in zip((pool.k_data, pool.v_data, pool.k_scale, pool.v_scale), want):
+        assert torch.equal(t, w)
