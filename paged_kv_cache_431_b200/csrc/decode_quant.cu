@@ -749,12 +749,15 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
 template <int DT, int D, bool RAG>
 int launch_q(const DecodeParams& p, int nht, dim3 grid, cudaStream_t s, const CUtensorMap* tmk, const CUtensorMap* tmv)
 {
-    const int smem = QCfg<DT, D>::BODY + 1024 + (p.part_tokens / kBlock) * (int)(sizeof(float2) + sizeof(int));
+    // by the partition, which differs from call to call: below the 48 KB that a kernel may have unasked, so
+    // no attribute is set, which calls of other threads would set to theirs before this launch
+    constexpr int kPerTile = (int)(sizeof(float2) + sizeof(int)), kMaxTiles = 4096 / kBlock;
+    static_assert(QCfg<DT, D>::BODY + 1024 + kMaxTiles * kPerTile <= 48 * 1024, "more than a kernel may have unasked");
+    if (p.part_tokens > kMaxTiles * kBlock) return PKV_ERR_ARG;
+    const int smem = QCfg<DT, D>::BODY + 1024 + (p.part_tokens / kBlock) * kPerTile;
     auto k1 = decode_mmaq_kernel<DT, D, 1, RAG>;
     auto k2 = decode_mmaq_kernel<DT, D, 2, RAG>;
     auto kern = nht == 1 ? k1 : k2;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return PKV_ERR_CUDA;
     if (p.rg.beside) {   // scheduled while the prefix pass runs (ragged_beside in the kernel)
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = grid;
