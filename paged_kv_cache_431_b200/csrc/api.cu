@@ -872,18 +872,21 @@ int paged_cross_attn(pkv_pool_t pool, int layer, const void* q, int q_dtype, con
     return launch_ragged_merge(a, s);
 }
 
-// The prefix pass of a grouped decode: where the suffixes, which run beside it, weigh more (their
-// bytes at HBM rate against the prefix tiles at about 2 us each), it is split for half the SMs, so that
-// both run side by side (8 prompts of 4,000 tokens, 32 sequences of up to 500 more on each: 122 -> 108 us).
+// The prefix pass of a grouped decode: where the suffixes run beside it (at the warp level) and weigh more
+// (their bytes at HBM rate against the prefix tiles at about 2 us each), it is split for half the SMs, so
+// that both run side by side (8 prompts of 4,000 tokens, 32 sequences of up to 500 more on each:
+// 122 -> 108 us).  Suffixes on tcgen05 come after it, and it has all SMs.
 static RaggedSplit prefix_split(pkv_pool_t pool, int num_groups, int max_group_size, int G, int max_prefix_len,
-                                int num_seqs, int max_suffix_len)
+                                int num_seqs, int max_suffix_len, const RaggedSplit& own)
 {
     const pkv_pool_desc& d = pool->d;
+    const double mean = (double)num_seqs / num_groups;
+    if (own.tc) return ragged_split(pool, num_groups, max_group_size, mean, G, max_prefix_len);
     const double rows = (double)max_group_size * G;
     const double tiles = (double)num_groups * d.num_kv_heads * ((rows + 255) / 256) * ((max_prefix_len + 127) / 128);
     const double prefix_us = tiles * 2.2 / num_sms();
     const double suffix_us = (double)num_seqs * max_suffix_len * d.num_kv_heads * 2 * pool->row_bytes / 6.5e6;
-    return ragged_split(pool, num_groups, max_group_size, (double)num_seqs / num_groups, G, max_prefix_len,
+    return ragged_split(pool, num_groups, max_group_size, mean, G, max_prefix_len,
                         suffix_us > prefix_us ? (num_sms() + 1) / 2 : num_sms());
 }
 
@@ -894,10 +897,10 @@ size_t paged_decode_groups_workspace_bytes(pkv_pool_t pool, int num_seqs, int nu
         max_group_size < 0 || max_prefix_len < 0 || max_suffix_len < 0)
         return 0;
     const int G = num_q_heads / pool->d.num_kv_heads;
+    const RaggedSplit own = ragged_split(pool, num_seqs, 1, 1., G, max_suffix_len);
     const int pre = max_prefix_len > 0 ? prefix_split(pool, num_groups, max_group_size, G, max_prefix_len, num_seqs,
-                                                      max_suffix_len).parts : 0;
-    const int own = ragged_split(pool, num_seqs, 1, 1., G, max_suffix_len).parts;
-    return pre + own > 1 ? ragged_ws_bytes(pool, num_seqs, num_q_heads, pre + own) : 0;
+                                                      max_suffix_len, own).parts : 0;
+    return pre + own.parts > 1 ? ragged_ws_bytes(pool, num_seqs, num_q_heads, pre + own.parts) : 0;
 }
 
 int paged_decode_attn_groups(pkv_pool_t pool, int layer, const void* q, int q_dtype, const int32_t* block_tables,
@@ -918,10 +921,10 @@ int paged_decode_attn_groups(pkv_pool_t pool, int layer, const void* q, int q_dt
     if (!block_tables || !context_lens || !group_starts || !prefix_lens) return PKV_ERR_NULL;
     RaggedArgs a = ragged_args(pool, layer, q, q_dtype, num_q_heads, scale, num_seqs, block_tables, block_table_width,
                                context_lens, group_starts, out);
-    const RaggedSplit pre = max_prefix_len > 0 ? prefix_split(pool, num_groups, max_group_size, a.G, max_prefix_len,
-                                                              num_seqs, max_suffix_len)
-                                               : RaggedSplit{false, false, PKV_BLOCK_SIZE, 0};
     const RaggedSplit own = ragged_split(pool, num_seqs, 1, 1., a.G, max_suffix_len);
+    const RaggedSplit pre = max_prefix_len > 0 ? prefix_split(pool, num_groups, max_group_size, a.G, max_prefix_len,
+                                                              num_seqs, max_suffix_len, own)
+                                               : RaggedSplit{false, false, PKV_BLOCK_SIZE, 0};
     const int slots = pre.parts + own.parts;
     const size_t need = slots > 1 ? ragged_ws_bytes(pool, num_seqs, num_q_heads, slots) : 0;
     if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15)))

@@ -83,3 +83,17 @@ def test_workspaces(pools):  # noqa: F811
 
 def test_descriptor_of_the_rotation_matches_the_header():
     assert ctypes.sizeof(pkv._Rope) == 24
+
+
+@pytest.mark.parametrize("groups_,size,prefix,suffix,same", [(4, 16, 8000, 8000, True), (8, 8, 8000, 8000, True),
+                                                             (8, 100, 4000, 500, False)])
+def test_prefix_pass_has_all_sms_unless_the_suffixes_run_beside_it(pools, groups_, size, prefix, suffix, same):  # noqa: F811
+    """Suffixes on tcgen05 (few long ones) come after the prefix pass, which is then split as a cross
+    attention of the same rows would be; lighter ones at the warp level run beside it, and where they weigh
+    more the prefix pass is split for fewer SMs.  The partitions are read off the workspaces."""
+    L, p, H_q, n = pkv.lib(), pools(pkv.BF16), 16, groups_ * size
+    row = n * H_q * (128 + 2) * 4
+    pre = max(1, L.paged_cross_workspace_bytes(p, n, H_q, groups_, size, prefix) // row)
+    own = max(1, L.paged_cross_workspace_bytes(p, n, H_q, n, 1, suffix) // row)
+    both = L.paged_decode_groups_workspace_bytes(p, n, H_q, groups_, size, prefix, suffix) // row
+    assert (both == pre + own) == same
