@@ -74,7 +74,7 @@ extern "C" {
 /* device status bits (OR-ed into pkv_pool_desc.device_status) */
 #define PKV_DEV_BAD_BLOCK   0x1  /* block table entry outside [0, num_blocks)           */
 #define PKV_DEV_BAD_SLOT    0x2  /* slot_mapping entry >= num_blocks * 16               */
-#define PKV_DEV_BAD_LENGTH  0x4  /* context_len < 0, > 16 * table width, or > max_context_len */
+#define PKV_DEV_BAD_LENGTH  0x4  /* context_len < 0, > 16 * table width, or past what max_context_len covers */
 #define PKV_DEV_TIMEOUT     0x8  /* a bounded wait on a bulk copy ran out               */
 #define PKV_DEV_BAD_PREFIX  0x10 /* cascade decode: a table does not start with the shared prefix */
 #define PKV_DEV_BAD_POSITION 0x20 /* kv_append_rope: a position outside the rotation's table */
@@ -248,7 +248,9 @@ PKV_API size_t paged_decode_workspace_bytes(pkv_pool_t pool, int num_seqs, int n
  *   block_tables [device]: int32 [num_seqs][block_table_width]; entries at index >=
  *        ceil(context_len / 16) are never read.  Entries may repeat across sequences.
  *   context_lens [device]: int32 [num_seqs], each <= max_context_len and <= 16 * width.
- *   max_context_len [host]: sizes the split-K grid.
+ *   max_context_len [host]: sizes the split-K grid.  (The device sees lengths past the grid's whole
+ *        partitions: one between max_context_len and the end of the partition that holds it is attended
+ *        to whole and not reported.)
  *   out [device]: fp32 [num_seqs][num_q_heads][head_dim].
  *   workspace [device]: paged_decode_workspace_bytes(...) bytes, 16-byte aligned.
  * num_q_heads / num_kv_heads must be an integer G >= 1 (MHA G = 1 .. MQA H_kv = 1; groups
@@ -344,7 +346,7 @@ PKV_API size_t paged_decode_groups_workspace_bytes(pkv_pool_t pool, int num_seqs
  *   prefix_lens [device]: int32 [num_groups], multiples of 16; 0: the group shares nothing.
  *   max_group_size, max_prefix_len, max_suffix_len [host]: bounds of a group's sequences, of
  *        prefix_lens, and of context_len - prefix_len (the lengths together at most 2^30); they size
- *        the grids.
+ *        the grids.  max_suffix_len counts in whole blocks (rounded up to a multiple of 16).
  *   workspace [device]: paged_decode_groups_workspace_bytes(...) bytes, 16-byte aligned.
  * All pool dtypes, head dims and group sizes.  On the device: lengths and group_starts out of
  * range are clipped to the bounds and set PKV_DEV_BAD_LENGTH; a prefix that is no multiple of 16
@@ -377,7 +379,7 @@ PKV_API size_t paged_cross_workspace_bytes(pkv_pool_t pool, int total_rows, int 
  *        no rows; rows of no sequence (behind the last) are padding, their output is left as it is.
  *   block_tables, context_lens [device]: as paged_decode_attn.
  *   max_rows, max_context_len [host]: bounds of a sequence's rows and of context_lens (the latter
- *        at most 2^30).
+ *        at most 2^30, and counted in whole blocks: rounded up to a multiple of 16).
  *   workspace [device]: paged_cross_workspace_bytes(...) bytes, 16-byte aligned.
  * Quantized pools: V scales of one sequence and KV head may differ by factors up to 2^20 without loss; a
  * row whose weight lies on blocks with smaller ones loses bits (a weight times its V scale is held in steps

@@ -862,6 +862,7 @@ int paged_cross_attn(pkv_pool_t pool, int layer, const void* q, int q_dtype, con
     a.mode = 0;   // kCross
     a.items = a.starts = num_seqs;
     a.max_rows = max_rows;
+    a.max_tokens = max_context_len;
     a.part_tokens = sp.part;
     a.max_parts = a.slots = sp.parts;
     a.ws_o = need ? static_cast<float*>(workspace) : nullptr;
@@ -942,6 +943,7 @@ int paged_decode_attn_groups(pkv_pool_t pool, int layer, const void* q, int q_dt
         a.mode = 1;   // kPrefix
         a.items = num_groups;
         a.max_rows = max_group_size;
+        a.max_tokens = max_prefix_len;
         a.part_tokens = pre.part;
         a.max_parts = pre.parts;
         rc = launch_ragged(pool, layer, a, pre, s);
@@ -951,6 +953,7 @@ int paged_decode_attn_groups(pkv_pool_t pool, int layer, const void* q, int q_dt
     a.mode = 2;   // kSuffix
     a.items = num_seqs;
     a.max_rows = 1;
+    a.max_tokens = max_suffix_len;
     a.part_tokens = own.part;
     a.max_parts = own.parts;
     a.part_base = pre.parts;

@@ -81,7 +81,7 @@ decode_mma16_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm
     const int32_t* trow;
     if constexpr (RAG) {
         if (ragged_beside(p.rg)) return;
-        it = ragged_item(p.rg, p.ctx_lens, p.W, p.max_parts * p.part_tokens, b, p.status,
+        it = ragged_item(p.rg, p.ctx_lens, p.W, b, p.status,
                          threadIdx.x == 0 && part == 0 && blockIdx.y == 0);
         GC = min(16, it.rows * p.G - 16 * hg);   // query rows of this warp
         ctx = it.end;
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(32 * kMergeHeads) ragged_merge_kernel(const De
     bool whole = true;
     if (item < 0 || h >= p.H_q) {
     } else if (r.mode == kSuffix) {
-        const RaggedItem it = ragged_item(r, p.ctx_lens, p.W, p.max_parts * p.part_tokens, t, p.status, false);
+        const RaggedItem it = ragged_item(r, p.ctx_lens, p.W, t, p.status, false);
         pre = (it.base + r.pre_part - 1) / r.pre_part;
         own = (it.end - it.base + p.part_tokens - 1) / p.part_tokens;
         whole = it.whole;
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(32 * kMergeHeads) ragged_merge_kernel(const De
     } else {
         int row0, rows;
         item_rows(r, item, row0, rows, p.status, false);
-        const RaggedItem it = ragged_item(r, p.ctx_lens, p.W, p.max_parts * p.part_tokens, item, p.status, false);
+        const RaggedItem it = ragged_item(r, p.ctx_lens, p.W, item, p.status, false);
         if (t < row0 + rows) own = (it.end + p.part_tokens - 1) / p.part_tokens;   // else: beyond the grid
     }
     pdl_wait_primary();   // the partials of the kernels before this one
@@ -822,6 +822,7 @@ static DecodeParams ragged_params(const RaggedArgs& a)
     p.rg.items = a.starts;
     p.rg.total_rows = a.total_rows;
     p.rg.max_rows = a.max_rows;
+    p.rg.max_tokens = (a.max_tokens + kBlock - 1) / kBlock * kBlock;
     p.rg.max_prefix = a.max_prefix;
     p.rg.pre_part = a.pre_part;
     p.rg.max_group = a.max_group;

@@ -34,6 +34,7 @@ struct RaggedParams {
     const int32_t* prefix_lens;   // [groups] (kPrefix, kSuffix)
     int items;                    // row_starts has items + 1 entries
     int total_rows, max_rows;     // rows of q; rows of an item that the grid covers
+    int max_tokens;               // the caller's bound of an item's keys, in whole blocks (the grid covers it)
     int max_prefix;               // kPrefix, kSuffix: tokens of a prefix that the grid covers
     int pre_part;                 // kSuffix's merge: tokens per prefix partition
     int max_group;                // kSuffix: sequences of a group that the prefix pass covered
@@ -152,8 +153,8 @@ __device__ __forceinline__ int item_of_row(const RaggedParams& r, int t)
 }
 
 // Item b of the launch (one whole warp asks).  rows 0: nothing to do.
-__device__ __forceinline__ RaggedItem ragged_item(const RaggedParams& r, const int32_t* ctx_lens, int W, int max_tokens,
-                                                  int b, int32_t* status, bool report)
+__device__ __forceinline__ RaggedItem ragged_item(const RaggedParams& r, const int32_t* ctx_lens, int W, int b,
+                                                  int32_t* status, bool report)
 {
     RaggedItem it;
     it.base = 0;
@@ -172,7 +173,7 @@ __device__ __forceinline__ RaggedItem ragged_item(const RaggedParams& r, const i
         it.table = it.whole ? b : it.row0;
         it.end = it.rows == 0 ? 0 : it.whole ? ctx_lens[b] : group_prefix(r, W, b, status, report);
     }
-    const int cap = min(W * kBlock, it.base + max_tokens);
+    const int cap = min(W * kBlock, it.base + r.max_tokens);
     if (it.end < it.base || it.end > cap) {
         if (report) flag_status(status, PKV_DEV_BAD_LENGTH);
         it.end = it.end < it.base ? it.base : cap;

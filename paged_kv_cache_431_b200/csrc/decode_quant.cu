@@ -290,7 +290,7 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
     const int32_t* trow;
     if constexpr (RAG) {
         if (ragged_beside(p.rg)) return;
-        it = ragged_item(p.rg, p.ctx_lens, p.W, p.max_parts * p.part_tokens, b, p.status,
+        it = ragged_item(p.rg, p.ctx_lens, p.W, b, p.status,
                          lane == 0 && part == 0 && blockIdx.y == 0);
         GC = min(16, it.rows * p.G - 16 * hg);   // query rows of this CTA
         ctx = it.end;

@@ -162,6 +162,7 @@ struct RaggedArgs {
     int H_q, H_kv, G, N, d, kv_dtype;
     int part_tokens, max_parts;
     int part_base, slots;   // first workspace slot of this launch, slots per row
+    int max_tokens;         // bound of an item's keys, from its base
     int max_prefix, pre_part, max_group;
     int beside;             // run beside the launch before it (a suffix pass beside its prefix pass)
     float scale;

@@ -228,7 +228,7 @@ ragged_tc_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK, 
     const int g = blockIdx.y;
     const int zparts = PAIR ? (p.max_parts + 1) / 2 : p.max_parts;
     const int b = blockIdx.z / zparts, z = blockIdx.z % zparts;
-    const RaggedItem it = ragged_item(p.rg, p.ctx_lens, p.W, p.max_parts * p.part_tokens, b, p.status,
+    const RaggedItem it = ragged_item(p.rg, p.ctx_lens, p.W, b, p.status,
                                       threadIdx.x == 0 && blockIdx.x == 0 && z == 0 && g == 0);
     const int R = it.rows * p.G;                                  // query rows of this KV head
     const int r0 = blockIdx.x * (C::QT * kBM);

@@ -165,3 +165,40 @@ def test_decode_of_small_and_large_pools(dt, d, H_q, H_kv, spread):
     for part in (0, 512):
         out = pkv.paged_decode_attn(pool, 0, q.to(DEV), tables.to(DEV), lens.to(DEV), scale, max(ctx), partition_tokens=part)
         assert np.abs(out.cpu().double().numpy() - ref).max() <= 2e-3 * spread
+
+
+@pytest.mark.parametrize("rows", [[2, 1], [7, 3], [25, 9], [90, 40]], ids=lambda r: f"{r[0]}rows")
+@pytest.mark.parametrize("dt", [pkv.BF16, pkv.INT8], ids=lambda x: NAMES[x])
+def test_cross_lengths_past_the_bound(dt, rows):
+    """max_context_len counts in whole blocks, whatever kernel and partition the shape gets: one token past
+    them is reported and left out, up to them nothing is."""
+    ctx = [305, 304]
+    pool, _, q, _, tables = cross.case(dt, 128, 4, 1, rows, ctx, 8500 + dt + rows[0])
+
+    def at(lens, bound):
+        out = pkv.paged_cross_attn(pool, 0, q.to(DEV), cross.starts_of(rows).to(DEV), tables.to(DEV),
+                                   torch.tensor(lens, dtype=torch.int32, device=DEV), 0.1, max(rows), bound)
+        torch.cuda.synchronize()
+        return out, pkv.read_device_status(pool)
+    for bound in (289, 304):
+        whole, status = at([304, 304], bound)
+        assert status == 0
+        clipped, status = at(ctx, bound)
+        assert status == pkv.DEV_BAD_LENGTH and torch.equal(clipped, whole)
+
+
+@pytest.mark.parametrize("H_q", [8, 64], ids=["warp_level", "tcgen05"])
+def test_groups_suffixes_past_the_bound(H_q):
+    from tests import test_gpu_groups as groups
+    sizes, prefix, suffix = [3, 2], [64, 32], [33, 20, 32, 1, 33]
+    pool, _, q, _, tables, ctx = groups.case(pkv.BF16, 128, H_q, 2, sizes, prefix, suffix, 8600 + H_q)
+
+    def at(lens, bound):
+        out = groups.call(pool, q, tables, lens, sizes, prefix, [bound] * 5, 0.1)
+        torch.cuda.synchronize()
+        return out, pkv.read_device_status(pool)
+    for bound in (17, 32):
+        whole, status = at([96, 84, 96, 33, 64], bound)
+        assert status == 0
+        clipped, status = at(ctx, bound)
+        assert status == pkv.DEV_BAD_LENGTH and torch.equal(clipped, whole)
