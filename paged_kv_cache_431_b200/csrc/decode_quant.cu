@@ -349,7 +349,9 @@ decode_mmaq_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmK
         vs_max = fmaxf(vs_max, tsc[j].y);
     }
     float v_up = pow2f(pow2_shift(warp_max(vs_max)));
-    asm volatile("" : "+f"(v_up));   // kept, not computed anew in the loop (ragged int4 119.3 -> 117.3 us)
+    // ragged form: kept, not computed anew in the loop (int4, 12 rows, 119.3 -> 117.3 us; the plain int4
+    // decode is scheduled worse so: 253.4 -> 258.4)
+    if constexpr (RAG) asm volatile("" : "+f"(v_up));
     if (lane == 0) {
         for (int s = 0; s < STAGES; ++s) mbar_init(smem_u32(&bars[s]), 1);
         mbar_fence_init();
