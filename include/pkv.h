@@ -348,6 +348,7 @@ PKV_API size_t paged_decode_groups_workspace_bytes(pkv_pool_t pool, int num_seqs
  *        prefix_lens, and of context_len - prefix_len (the lengths together at most 2^30); they size
  *        the grids.  max_suffix_len counts in whole blocks (rounded up to a multiple of 16).
  *   workspace [device]: paged_decode_groups_workspace_bytes(...) bytes, 16-byte aligned.
+ * Scores that are not finite and V scales far apart: as paged_cross_attn.
  * All pool dtypes, head dims and group sizes.  On the device: lengths and group_starts out of
  * range are clipped to the bounds and set PKV_DEV_BAD_LENGTH; a prefix that is no multiple of 16
  * (it counts rounded down) or a table without its group's prefix sets PKV_DEV_BAD_PREFIX.
@@ -381,6 +382,7 @@ PKV_API size_t paged_cross_workspace_bytes(pkv_pool_t pool, int total_rows, int 
  *   max_rows, max_context_len [host]: bounds of a sequence's rows and of context_lens (the latter
  *        at most 2^30, and counted in whole blocks: rounded up to a multiple of 16).
  *   workspace [device]: paged_cross_workspace_bytes(...) bytes, 16-byte aligned.
+ * A score of NaN or +inf makes its row NaN, one of -inf weighs nothing; NaN in V reaches its dim.
  * Quantized pools: V scales of one sequence and KV head may differ by factors up to 2^20 without loss; a
  * row whose weight lies on blocks with smaller ones loses bits (a weight times its V scale is held in steps
  * of at most 2^-30 of the largest V scale).
